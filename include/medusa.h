@@ -70,6 +70,7 @@ extern "C" {
 #define MEDUSA_MAX_K 8    /* tree depth / Medusa heads */
 #define MEDUSA_MAX_S 16   /* top-s per head */
 #define MEDUSA_MAX_B 16   /* sequences per call */
+#define MEDUSA_MAX_ROWS 1024 /* rows of a paged cache, and its batch */
 
 typedef enum { MEDUSA_F32 = 0, MEDUSA_BF16 = 1 } medusa_dtype;
 
@@ -88,7 +89,9 @@ enum {
   MEDUSA_DEVERR_NODE = 2,     /* node index outside [0, T) */
   MEDUSA_DEVERR_CAPACITY = 4, /* prefix_len + T exceeds seq_cap */
   MEDUSA_DEVERR_LENGTH = 8,   /* accept_len outside [0, K] */
-  MEDUSA_DEVERR_TIMEOUT = 16  /* a bounded on-chip wait gave up (internal fault) */
+  MEDUSA_DEVERR_TIMEOUT = 16, /* a bounded on-chip wait gave up (internal fault) */
+  MEDUSA_DEVERR_PAGE = 32,    /* a page outside the pool, or a row's state that contradicts itself */
+  MEDUSA_DEVERR_ROW = 64      /* a cache row outside its range, named twice or not empty */
 };
 
 typedef struct medusa_tree {
@@ -583,6 +586,183 @@ int medusa_append_tokens(const int32_t* tokens, const int32_t* accepted_nodes,
 int medusa_standin_embed(const int32_t* tokens, int rows, const void* emb,
                          int V, int d, medusa_dtype dtype, void* hidden,
                          int32_t* err, void* stream);
+
+/* ============================== paged cache ============================== */
+
+/* A key/value cache in pages, for many sequences that come, go and share
+ * prefixes.  The data lie in pools k_pages, v_pages, device
+ * [num_pages][Hkv][page_size][Dh] (one pair per layer), and the bookkeeping,
+ * common to all layers, in this struct's arrays.  Row r holds length[r]
+ * tokens in held[r] pages table[r][0 .. held[r]-1]; its token x lies in page
+ * table[r][x / page_size], line x % page_size.  Rows may share pages: refs[p]
+ * counts the rows that hold page p; free_bits has bit p % 32 of word p / 32
+ * set iff refs[p] is 0.  The calls below keep that; a caller reads the arrays,
+ * may copy all of them to go back to an earlier state, and otherwise changes
+ * them through the calls.
+ * page_size is 16, 32, 64, 128 or 256; rows at most MEDUSA_MAX_ROWS;
+ * num_pages at most 2^26; num_pages * Hkv * page_size below 2^31.
+ *
+ * A decode step of a batch:
+ *   medusa_pages_reserve   room for each row's new tokens; its list of copies
+ *   medusa_pages_copy      ... carried out, once per layer
+ *   medusa_paged_attn      once per layer: append, attend
+ *   medusa_paged_compact   once per layer, after a tree: the accepted path
+ *   medusa_pages_commit    the rows' new lengths
+ * medusa_pages_fork starts a row that continues another one's tokens,
+ * medusa_pages_free ends a row or cuts it back, medusa_pages_compact moves the
+ * live pages to the front of the pool.  The paper's step has no counterpart:
+ * it keeps one dense slab per sequence (medusa_tree_attn). */
+typedef struct medusa_pages {
+  int32_t* refs;       /* device [num_pages] */
+  uint32_t* free_bits; /* device [ceil(num_pages / 32)]; bits past num_pages 0 */
+  int32_t* length;     /* device [rows]: tokens */
+  int32_t* held;       /* device [rows]: pages */
+  int32_t* table;      /* device [rows][max_pages]; -1 past held[r] */
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t rows;
+  int32_t max_pages; /* pages a row may hold */
+} medusa_pages_t;
+
+/* The empty cache: every page free, every row without tokens. */
+int medusa_pages_init(const medusa_pages_t* pages, void* stream);
+
+/* Give rows back, wholly or from a token on.  keep_len: device [rows]; a row
+ * with keep_len[r] < 0 is left alone, any other keeps its first
+ * min(length[r], keep_len[r]) tokens and the pages they lie in, and loses the
+ * rest (pages reserved past its length too).  A page nobody holds any more is
+ * free.  A held page outside the pool or without references sets
+ * MEDUSA_DEVERR_PAGE and is only taken out of the row. */
+int medusa_pages_free(const medusa_pages_t* pages, const int32_t* keep_len,
+                      int32_t* err, void* stream);
+
+/* Row dst[i] becomes a second holder of row src[i]'s tokens (not of pages
+ * reserved past them), i < n <= MEDUSA_MAX_ROWS.  src, dst: device [n].  A
+ * source may occur many times; a destination must be an empty row.  An entry
+ * with a row out of range, a destination that is not empty or was named
+ * before, or a row that occurs both as a source and as a destination sets
+ * MEDUSA_DEVERR_ROW and is skipped. */
+int medusa_pages_fork(const medusa_pages_t* pages, const int32_t* src,
+                      const int32_t* dst, int n, int32_t* err, void* stream);
+
+/* Room for n_new[r] more tokens in every row (device [rows]; 0 asks for
+ * nothing).  Rows are served in order, with the lowest free pages: a row needs
+ * the pages its new length lacks and, where its last page is partly filled and
+ * shared, one for a copy of that page, so that it alone writes there (of the
+ * rows in this call that are a page's only holders, the last keeps the page).
+ * A row is served iff what it and all rows before it need is there; otherwise
+ * it and the rows after it stay as they were, and those that asked for tokens
+ * set MEDUSA_DEVERR_CAPACITY.  granted [rows] (nullable): 1 or 0.  A row past
+ * max_pages (MEDUSA_DEVERR_CAPACITY), with n_new < 0 (MEDUSA_DEVERR_LENGTH) or
+ * a broken state (MEDUSA_DEVERR_PAGE) needs nothing and is not served.
+ * copies: device [max_copies][4], 16-byte aligned, max_copies >= rows: line i
+ * says {source page, destination page, tokens, row} in row order, for
+ * medusa_pages_copy; *n_copies (device) says how many; later lines are left.
+ * length stays: medusa_pages_commit moves it. */
+int medusa_pages_reserve(const medusa_pages_t* pages, const int32_t* n_new,
+                         int32_t* copies, int max_copies, int32_t* n_copies,
+                         int32_t* granted, int32_t* err, void* stream);
+
+/* length[rows[b]] += n_new[b] + bias for b < B (rows, n_new: device [B]; rows
+ * NULL: row b).  After a chunk bias is 0; after a verified tree n_new is
+ * accept_len and bias 1.  A row out of range or named before sets
+ * MEDUSA_DEVERR_ROW, n_new < 0 MEDUSA_DEVERR_LENGTH, a length past the row's
+ * pages MEDUSA_DEVERR_CAPACITY; the entry is skipped. */
+int medusa_pages_commit(const medusa_pages_t* pages, const int32_t* rows,
+                        const int32_t* n_new, int bias, int B, int32_t* err,
+                        void* stream);
+
+/* Scratch bytes medusa_pages_compact needs. */
+size_t medusa_pages_compact_workspace_size(int num_pages);
+
+/* Live pages to the front: with n of them, the i-th live page at or past n
+ * goes to the i-th free page below n, in every row that holds it.  refs,
+ * free_bits and table say so at once; copies (as medusa_pages_reserve's, in
+ * source order, tokens = page_size, row = -1) is for medusa_pages_copy, which
+ * has to follow before anything reads or writes the pools.  More than
+ * max_copies moves: MEDUSA_DEVERR_CAPACITY, *n_copies = 0, nothing changes. */
+int medusa_pages_compact(const medusa_pages_t* pages, int32_t* copies,
+                         int max_copies, int32_t* n_copies, void* workspace,
+                         size_t workspace_bytes, int32_t* err, void* stream);
+
+/* Carry out a list of copies in one layer's pools: the first `tokens` lines of
+ * every head of the source page into the destination page.  Sources and
+ * destinations must be distinct pages, as the two calls that write such lists
+ * see to.  A line with a page outside the pool or tokens outside
+ * [0, page_size] sets MEDUSA_DEVERR_PAGE and is skipped; *n_copies above
+ * max_copies sets MEDUSA_DEVERR_CAPACITY and stops there.  Dh 64 or 128. */
+int medusa_pages_copy(void* k_pages, void* v_pages, int num_pages,
+                      int page_size, int Hkv, int Dh, medusa_dtype dtype,
+                      const int32_t* copies, const int32_t* n_copies,
+                      int max_copies, int32_t* err, void* stream);
+
+/* Scratch bytes medusa_paged_attn needs (current device). */
+size_t medusa_paged_attn_workspace_size(int B, int total_q, int max_new, int H,
+                                        int Hkv, int Dh, medusa_dtype dtype);
+
+/* Attention of a chunk of new tokens per sequence over the paged cache: the
+ * prefix's chunks, single tokens, and verification trees.
+ *   q:            device, token t's H heads of Dh at q + t * q_stride;
+ *   k_new, v_new: device, token t's Hkv heads at + t * k_stride / v_stride
+ *                 (strides in elements: the three may be parts of one
+ *                 projection's output), all before rotation;
+ *   q_start:      device [B+1], q_start[0] >= 0, not decreasing,
+ *                 q_start[B] <= total_q: sequence b's tokens are rows
+ *                 q_start[b] .. q_start[b+1]-1, n_b of them, possibly none;
+ *                 rows outside every sequence are neither read nor written;
+ *   rows:         device [B], sequence b's cache row (NULL: row b);
+ *   max_new:      host bound on every n_b;
+ *   tree:         NULL: causal; else every n_b is 0 or tree->T.
+ * For token i of sequence b with L = length[rows[b]], query head h reads key
+ * head h / (H / Hkv):
+ *   pos = L + i (causal) or L + depth_i (tree);
+ *   k' = RoPE(k_new, pos) and v_new are written at row token L + i;
+ *   out = softmax(scale * RoPE(q, pos) . K^T) V over row tokens 0 .. L + i
+ *   (causal), or the prefix and L + j for every ancestor-or-self j (tree).
+ * RoPE as medusa_tree_attn (pairs (j, j + Dh/2)), the angle exact to 2^-30 of
+ * a turn at any position.  The cache is read as it is stored, in its type.
+ * A key that a token does not see has no effect on it, with one limit:
+ * non-finite values among a chunk's own v_new may reach other tokens of the
+ * same chunk.
+ * length stays (medusa_pages_commit); the pages for L + n_b tokens must be
+ * there and the last ones the row's own (medusa_pages_reserve).
+ * out: device [total_q][H][Dh].  H a multiple of Hkv, H / Hkv <= 64, Dh 64 or
+ * 128, B <= MEDUSA_MAX_ROWS; tensors 16-byte aligned, strides multiples of 16
+ * bytes.  A sequence whose row is out of range or was named before
+ * (MEDUSA_DEVERR_ROW), with n_b outside 0 .. max_new, another q_start fault or
+ * another n_b than the tree's (MEDUSA_DEVERR_LENGTH), whose pages do not cover
+ * L + n_b (MEDUSA_DEVERR_CAPACITY) or whose state is broken
+ * (MEDUSA_DEVERR_PAGE) is skipped.  A held page outside the pool sets
+ * MEDUSA_DEVERR_PAGE; it is not written and reads as zeros.
+ * The workspace holds arrival counters: zero-filled (cudaMemset) before its
+ * first call, left ready by every call, whatever the next call's sizes (zero
+ * it again after MEDUSA_DEVERR_TIMEOUT).  Calls that may overlap in time need
+ * workspaces of their own. */
+int medusa_paged_attn(const void* q, int64_t q_stride, const void* k_new,
+                      int64_t k_stride, const void* v_new, int64_t v_stride,
+                      void* k_pages, void* v_pages,
+                      const medusa_pages_t* pages, const int32_t* rows,
+                      const int32_t* q_start, int B, int total_q, int max_new,
+                      const medusa_tree_t* tree, int H, int Hkv, int Dh,
+                      float rope_theta, float scale, medusa_dtype dtype,
+                      void* out, void* workspace, size_t workspace_bytes,
+                      int32_t* err, void* stream);
+
+/* medusa_kv_compact inside pages, one layer: for sequence b with
+ * L = length[rows[b]] (rows NULL: row b) and A = accept_len[b],
+ *   row token L + j <- row token L + accepted_nodes[b][j], j = 0 .. A
+ * (every source is read before any destination is written).  length stays, so
+ * that the next layer's call finds the same L: medusa_pages_commit with
+ * n_new = accept_len and bias 1 follows the last one.  accepted_nodes: device
+ * [B][Kmax+1], accept_len: device [B], Kmax <= MEDUSA_MAX_K, T: the tree's
+ * rows.  MEDUSA_DEVERR_LENGTH, _NODE, _ROW, _CAPACITY (a node past the row's
+ * pages) and _PAGE as above; such a sequence is left untouched. */
+int medusa_paged_compact(void* k_pages, void* v_pages,
+                         const medusa_pages_t* pages, const int32_t* rows,
+                         const int32_t* accepted_nodes,
+                         const int32_t* accept_len, int B, int Hkv, int Dh,
+                         int Kmax, int T, medusa_dtype dtype, int32_t* err,
+                         void* stream);
 
 #ifdef __cplusplus
 }

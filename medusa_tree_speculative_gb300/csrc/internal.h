@@ -19,6 +19,11 @@ int check_launch(const char* what);
 int sm_count();
 // Validate a medusa_tree_t (host fields and non-null device arrays).
 int check_tree(const medusa_tree_t* tree, const char* what);
+// Validate a medusa_pages_t (host fields and non-null device arrays).
+int check_pages(const medusa_pages_t* pages, const char* what);
+// Validate the pools of a paged cache.
+int check_pool(const void* k_pages, const void* v_pages, int num_pages, int page_size, int Hkv, int Dh,
+               medusa_dtype dtype, const char* what);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

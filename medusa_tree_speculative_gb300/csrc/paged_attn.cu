@@ -1,0 +1,472 @@
+// Chunk attention over the paged cache: the call, the rotation and append of a
+// chunk, and the kernels on the CUDA cores.
+#include <cmath>
+
+#include "paged_attn.cuh"
+
+namespace medusa {
+namespace {
+
+// ------------------------------------------------ rotate, scale, append --
+// A CTA per kPrepTokens tokens: cos and sin of a token's position once per
+// pair, in shared memory, then eight pairs per thread and step.  Queries go to
+// q_rot with the softmax scale in them, keys and values to their pages.  Bound
+// by memory: every element is read and written once.
+constexpr int kPrepTokens = 4;
+constexpr int kPrepThreads = 256;
+
+template <typename T>
+MDEV void load8(const T* p, float* f);
+template <>
+MDEV void load8<float>(const float* p, float* f) {
+  const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+  f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+  f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+}
+template <>
+MDEV void load8<uint16_t>(const uint16_t* p, float* f) {
+  unpack8_bf16(*reinterpret_cast<const uint4*>(p), f);
+}
+template <typename T>
+MDEV void store8(T* p, const float* f);
+template <>
+MDEV void store8<float>(float* p, const float* f) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+}
+template <>
+MDEV void store8<uint16_t>(uint16_t* p, const float* f) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_constant__ PagedAttnArgs a) {
+  __shared__ float cs[kPrepTokens][DH / 2], sn[kPrepTokens][DH / 2];
+  __shared__ int64_t line0[kPrepTokens];  // head 0's line of the token's slot, -1: no page
+  __shared__ int use[kPrepTokens], pos[kPrepTokens];
+  const int t = threadIdx.x, tok0 = blockIdx.x * kPrepTokens, nt = min(kPrepTokens, a.total_q - tok0);
+  for (int k = 0; k < nt; ++k) {
+    const int tok = tok0 + k;
+    int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before the token
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.q_start[mid] <= tok) lo = mid; else hi = mid - 1;
+    }
+    SeqInfo s;
+    int code;
+    bool ok = seq_info(a, lo, s, code) && tok >= s.q0 && tok < s.q0 + s.n;
+    const int64_t r = (int64_t)s.n * a.g;
+    ok = ok && r >= a.r_lo && r <= a.r_hi;
+    bool twice = false;
+    if (ok && a.rows)  // an entry whose row an earlier one names is skipped
+      for (int j = t; j < lo; j += kPrepThreads) twice |= a.rows[j] == s.row && a.q_start[j + 1] > a.q_start[j];
+    twice = __syncthreads_or(twice);
+    if (t == 0) {
+      ok = ok && !twice;
+      use[k] = ok;
+      pos[k] = 0;
+      line0[k] = -1;
+      if (ok) {
+        const int i = tok - s.q0;
+        pos[k] = s.L + (a.T ? min(max(a.depth[i], 0), a.K) : i);
+        const int page = page_of(a, s, s.L + i);
+        if (page >= 0) line0[k] = page_line(a.p, page, a.Hkv, 0, (s.L + i) & (a.p.page_size - 1));
+      }
+    }
+  }
+  __syncthreads();
+  for (int e = t; e < nt * (DH / 2); e += kPrepThreads)
+    rope_cos_sin(pos[e / (DH / 2)], a.turns[e % (DH / 2)], cs[e / (DH / 2)][e % (DH / 2)],
+                 sn[e / (DH / 2)][e % (DH / 2)]);
+  __syncthreads();
+  constexpr int kChunks = DH / 16;  // runs of eight pairs in a head
+  const int heads = a.H + 2 * a.Hkv, items = nt * heads * kChunks;
+  const T* q = static_cast<const T*>(a.q);
+  for (int e = t; e < items; e += kPrepThreads) {
+    const int c = e % kChunks, h = e / kChunks % heads, k = e / (kChunks * heads);
+    if (!use[k]) continue;
+    const int64_t tok = tok0 + k;
+    float lo[8], hi[8];
+    const T* src = h < a.H ? q + tok * a.q_stride + (int64_t)h * DH
+                   : h < a.H + a.Hkv ? static_cast<const T*>(a.k_new) + tok * a.k_stride + (int64_t)(h - a.H) * DH
+                                     : static_cast<const T*>(a.v_new) + tok * a.v_stride +
+                                           (int64_t)(h - a.H - a.Hkv) * DH;
+    T* dst;
+    if (h < a.H) {
+      dst = static_cast<T*>(a.q_rot) + (((int64_t)(h / a.g) * a.total_q + tok) * a.g + h % a.g) * DH;
+    } else {
+      if (line0[k] < 0) continue;
+      const int hk = h < a.H + a.Hkv ? h - a.H : h - a.H - a.Hkv;
+      dst = static_cast<T*>(h < a.H + a.Hkv ? a.k_pages : a.v_pages) +
+            (line0[k] + ((int64_t)hk << a.p.shift)) * DH;
+    }
+    load8(src + c * 8, lo);
+    load8(src + DH / 2 + c * 8, hi);
+    if (h < a.H + a.Hkv) {
+      const float mul = h < a.H ? a.qscale : 1.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float co = cs[k][c * 8 + j], si = sn[k][c * 8 + j], x = lo[j], y = hi[j];
+        lo[j] = (x * co - y * si) * mul;
+        hi[j] = (y * co + x * si) * mul;
+      }
+    }
+    store8(dst + c * 8, lo);
+    store8(dst + DH / 2 + c * 8, hi);
+  }
+}
+
+// -------------------------------------------------- CUDA-core kernel --
+// S = Q K^T and O += P V on the CUDA cores: 256 threads as 16 x 16, thread
+// (ty, tx) with rows ty + 16 a of the block, keys tx + 16 b of the tile and,
+// for O, columns tx * 4 + 64 c.  A row's sixteen threads are half a warp, so
+// its maximum and sum are four shuffles.  Key rows are padded by 16 bytes
+// (eight threads' 16-byte loads of eight rows then hit different banks).  The
+// value tile loads while S is computed and the next key tile while O is.
+constexpr int kGenThreads = 256;
+
+template <typename T, int DH, int RB, int KT>
+struct Gen {
+  static constexpr int TM = RB / 16, TN = KT / 16, CC = DH / 64;
+  static constexpr int kQ = RB * (DH + 4), kK = KT * (DH + 4), kV = KT * DH, kP = RB * (KT + 4);
+  static constexpr size_t smem = (size_t)(kQ + kK + kV + kP) * 4 + sizeof(PlanScratch) + sizeof(Plan) + 64;
+  static constexpr int part_floats = RB * DH + 2 * RB;
+};
+
+template <typename T, int DH, int RB, int KT>
+__global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid_constant__ PagedAttnArgs a) {
+  using G = Gen<T, DH, RB, KT>;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;                  // [RB][DH + 4]
+  float* Ks = Qs + G::kQ;          // [KT][DH + 4]
+  float* Vs = Ks + G::kK;          // [KT][DH]
+  float* Ps = Vs + G::kV;          // [RB][KT + 4]
+  PlanScratch& sc = *reinterpret_cast<PlanScratch*>(Ps + G::kP);
+  Plan& pl = *reinterpret_cast<Plan*>(&sc + 1);
+  int* flag = reinterpret_cast<int*>(&pl + 1);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  int64_t x, x1;
+  make_plan<kGenThreads, RB, KT>(a, sc, pl, x, x1);
+  if (x >= x1) return;
+  const int64_t total = pl.total, grid = min((int64_t)gridDim.x, total);
+  const int tb = RB / a.g;
+  Segment sg;
+  seek_segment<RB, KT>(a, sc, x, x1, sg);
+  while (true) {
+    const SeqInfo& s = sg.s;
+    const int nkeys = s.L + s.n, tok0 = sg.u * tb, live = min(tb, s.n - tok0) * a.g;
+    // one tile of keys or values, zeros where there is none
+    auto load = [&](const void* pool, float* dst, int stride, int t) {
+      constexpr int kVec = 16 / sizeof(T), kRow = DH / kVec;
+      for (int e = tid; e < KT * kRow; e += kGenThreads) {
+        const int key = t * KT + e / kRow, c = e % kRow;
+        const T* src = static_cast<const T*>(pool);
+        bool ok = key < nkeys;
+        if (ok) {
+          const int page = page_of(a, s, key);
+          ok = page >= 0;
+          if (ok) src += page_line(a.p, page, a.Hkv, sg.head, key & (a.p.page_size - 1)) * DH + c * kVec;
+        }
+        float* d = dst + (e / kRow) * stride + c * kVec;
+        if constexpr (sizeof(T) == 4) {
+          cp_async16(smem_u32(d), src, ok ? 16 : 0);
+        } else {
+          float f[8] = {};
+          if (ok) load8(src, f);
+          store8(d, f);
+        }
+      }
+      cp_async_commit();
+    };
+    __syncthreads();  // the previous segment's tiles are read
+    {
+      const T* qr = static_cast<const T*>(a.q_rot) +
+                    ((int64_t)sg.head * a.total_q + s.q0 + tok0) * a.g * (int64_t)DH;
+      for (int e = tid; e < RB * (DH / 8); e += kGenThreads) {
+        const int r = e / (DH / 8), c = e % (DH / 8);
+        float f[8] = {};
+        if (r < live) load8(qr + (int64_t)r * DH + c * 8, f);
+        store8(Qs + r * (DH + 4) + c * 8, f);
+      }
+    }
+    load(a.k_pages, Ks, DH + 4, sg.t0);
+    load(a.v_pages, Vs, DH, sg.t0);
+    float o[G::TM][G::CC * 4], m[G::TM], l[G::TM];
+#pragma unroll
+    for (int i = 0; i < G::TM; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < G::CC * 4; ++c) o[i][c] = 0.f;
+    }
+    for (int t = sg.t0; t < sg.t1; ++t) {
+      cp_async_wait<1>();  // this tile's keys
+      __syncthreads();
+      float z[G::TM][G::TN] = {};
+#pragma unroll 4
+      for (int d = 0; d < DH; d += 4) {
+        float4 qv[G::TM], kv[G::TN];
+#pragma unroll
+        for (int i = 0; i < G::TM; ++i) qv[i] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * (DH + 4) + d);
+#pragma unroll
+        for (int j = 0; j < G::TN; ++j) kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * (DH + 4) + d);
+#pragma unroll
+        for (int i = 0; i < G::TM; ++i)
+#pragma unroll
+          for (int j = 0; j < G::TN; ++j)
+            z[i][j] += qv[i].x * kv[j].x + qv[i].y * kv[j].y + qv[i].z * kv[j].z + qv[i].w * kv[j].w;
+      }
+      __syncthreads();  // the keys are read
+      if (t + 1 < sg.t1) load(a.k_pages, Ks, DH + 4, t + 1);
+      else cp_async_commit();
+      const bool masked = (t + 1) * KT > s.L;  // keys past the prefix: the mask decides
+#pragma unroll
+      for (int i = 0; i < G::TM; ++i) {
+        const int r = ty + 16 * i, tok = tok0 + r / a.g;
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < G::TN; ++j) {
+            const int key = t * KT + tx + 16 * j;
+            if (r >= live || key >= nkeys || !key_seen(a, s, tok, key)) z[i][j] = -INFINITY;
+          }
+        }
+        float mt = z[i][0];
+#pragma unroll
+        for (int j = 1; j < G::TN; ++j) mt = fmaxf(mt, z[i][j]);
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, w));
+        const float mn = fmaxf(m[i], mt), base = mn == -INFINITY ? 0.f : mn;
+        const float alpha = exp2f(m[i] - base);
+        m[i] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < G::TN; ++j) {
+          const float pj = exp2f(z[i][j] - base);
+          sum += pj;
+          Ps[r * (KT + 4) + tx + 16 * j] = pj;
+        }
+        l[i] = l[i] * alpha + sum;  // this thread's keys; the sixteen parts are added at the end
+#pragma unroll
+        for (int c = 0; c < G::CC * 4; ++c) o[i][c] *= alpha;
+      }
+      cp_async_wait<1>();  // this tile's values
+      __syncthreads();
+#pragma unroll 2
+      for (int k = 0; k < KT; k += 4) {
+        float4 pv[G::TM];
+#pragma unroll
+        for (int i = 0; i < G::TM; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * (KT + 4) + k);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          float4 vv[G::CC];
+#pragma unroll
+          for (int c = 0; c < G::CC; ++c)
+            vv[c] = *reinterpret_cast<const float4*>(Vs + (k + kk) * DH + tx * 4 + 64 * c);
+#pragma unroll
+          for (int i = 0; i < G::TM; ++i) {
+            const float pj = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
+#pragma unroll
+            for (int c = 0; c < G::CC; ++c) {
+              o[i][c * 4] += pj * vv[c].x;
+              o[i][c * 4 + 1] += pj * vv[c].y;
+              o[i][c * 4 + 2] += pj * vv[c].z;
+              o[i][c * 4 + 3] += pj * vv[c].w;
+            }
+          }
+        }
+      }
+      __syncthreads();  // the values are read
+      if (t + 1 < sg.t1) load(a.v_pages, Vs, DH, t + 1);
+      else cp_async_commit();
+    }
+#pragma unroll
+    for (int i = 0; i < G::TM; ++i)
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+    auto put = [&](int i, const float* v, float sum) {  // row ty + 16 i of the block
+      const int r = ty + 16 * i;
+      if (r >= live) return;
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      T* dst = static_cast<T*>(a.out) +
+               ((int64_t)(s.q0 + tok0 + r / a.g) * a.H + (int64_t)sg.head * a.g + r % a.g) * DH;
+#pragma unroll
+      for (int c = 0; c < G::CC; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dst[tx * 4 + 64 * c + j] = from_f32<T>(v[c * 4 + j] * inv);
+    };
+    if (sg.t0 == 0 && sg.t1 == sg.tiles) {
+#pragma unroll
+      for (int i = 0; i < G::TM; ++i) put(i, o[i], l[i]);
+    } else {
+      int first, last;
+      unit_shares(sg, total, grid, first, last);
+      float* mine = a.part + (int64_t)part_slot(sg.unit_x, blockIdx.x, total, grid) * G::part_floats;
+#pragma unroll
+      for (int i = 0; i < G::TM; ++i) {
+        const int r = ty + 16 * i;
+#pragma unroll
+        for (int c = 0; c < G::CC; ++c)
+          *reinterpret_cast<float4*>(mine + r * DH + tx * 4 + 64 * c) =
+              make_float4(o[i][c * 4], o[i][c * 4 + 1], o[i][c * 4 + 2], o[i][c * 4 + 3]);
+        if (tx == 0) *reinterpret_cast<float2*>(mine + RB * DH + 2 * r) = make_float2(m[i], l[i]);
+      }
+      __syncthreads();
+      if (tid == 0) {
+        const int before = arrive_acq_rel(a.counters + first);
+        *flag = before == last - first;
+        if (before == last - first) a.counters[first] = 0;  // ready for the next call
+      }
+      __syncthreads();
+      if (*flag) {
+#pragma unroll
+        for (int i = 0; i < G::TM; ++i) {
+          const int r = ty + 16 * i;
+          float M = -INFINITY, sum = 0.f, acc[G::CC * 4] = {};
+          for (int c = first; c <= last; ++c)
+            M = fmaxf(M, __ldcg(a.part + (int64_t)part_slot(sg.unit_x, c, total, grid) * G::part_floats + RB * DH +
+                                2 * r));
+          for (int c = first; c <= last; ++c) {
+            const float* pt = a.part + (int64_t)part_slot(sg.unit_x, c, total, grid) * G::part_floats;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pt + RB * DH + 2 * r));
+            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+            sum += w * ml.y;
+#pragma unroll
+            for (int cc = 0; cc < G::CC; ++cc) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(pt + r * DH + tx * 4 + 64 * cc));
+              acc[cc * 4] += w * v.x;
+              acc[cc * 4 + 1] += w * v.y;
+              acc[cc * 4 + 2] += w * v.z;
+              acc[cc * 4 + 3] += w * v.w;
+            }
+          }
+          put(i, acc, sum);
+        }
+      }
+    }
+    x += sg.t1 - sg.t0;
+    if (x >= x1) break;
+    next_segment<RB, KT>(a, pl, x, x1, sg);
+  }
+}
+
+template <typename T, int DH, int RB, int KT>
+int run_generic(const PagedAttnArgs& a, const PagedKernels& k) {
+  using G = Gen<T, DH, RB, KT>;
+  auto* fn = paged_generic_kernel<T, DH, RB, KT>;
+  cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::smem);
+  launch_kernel(fn, dim3(k.sms * 2), dim3(kGenThreads), G::smem, k.stream, a);
+  return check_launch("medusa_paged_attn");
+}
+
+template <typename T>
+int run_generic_t(const PagedAttnArgs& a, int Dh, bool few, const PagedKernels& k) {
+  if (few) return Dh == 64 ? run_generic<T, 64, 16, 64>(a, k) : run_generic<T, 128, 16, 64>(a, k);
+  return Dh == 64 ? run_generic<T, 64, 64, 32>(a, k) : run_generic<T, 128, 64, 32>(a, k);
+}
+
+// The workspace: both kernels' counters first, at the same place for every
+// size, then the rotated queries, then the partials.
+struct PagedWorkspace {
+  size_t q_rot, part, total;
+};
+constexpr size_t kCounterBytes = 2 * kPagedCounters * 4;
+
+PagedWorkspace workspace_of(int total_q, int H, int Dh, medusa_dtype dtype, int sms) {
+  PagedWorkspace w;
+  w.q_rot = kCounterBytes;
+  w.part = align_up(w.q_rot + (size_t)total_q * H * Dh * (dtype == MEDUSA_BF16 ? 2 : 4), 256);
+  w.total = align_up(w.part + (size_t)(sms * 2) * 2 * (64 * Dh + 2 * 64) * 4, 256);
+  return w;
+}
+
+}  // namespace
+
+int launch_paged_prep(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, const PagedKernels& k) {
+  const dim3 grid((a.total_q + kPrepTokens - 1) / kPrepTokens);
+  if (dtype == MEDUSA_BF16) {
+    if (Dh == 64) launch_kernel(paged_prep_kernel<uint16_t, 64>, grid, dim3(kPrepThreads), 0, k.stream, a);
+    else launch_kernel(paged_prep_kernel<uint16_t, 128>, grid, dim3(kPrepThreads), 0, k.stream, a);
+  } else {
+    if (Dh == 64) launch_kernel(paged_prep_kernel<float, 64>, grid, dim3(kPrepThreads), 0, k.stream, a);
+    else launch_kernel(paged_prep_kernel<float, 128>, grid, dim3(kPrepThreads), 0, k.stream, a);
+  }
+  return check_launch("medusa_paged_attn");
+}
+
+int launch_paged_generic(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, bool few_rows, const PagedKernels& k) {
+  return dtype == MEDUSA_BF16 ? run_generic_t<uint16_t>(a, Dh, few_rows, k) : run_generic_t<float>(a, Dh, few_rows, k);
+}
+
+}  // namespace medusa
+
+using namespace medusa;
+
+extern "C" size_t medusa_paged_attn_workspace_size(int B, int total_q, int max_new, int H, int Hkv, int Dh,
+                                                   medusa_dtype dtype) {
+  if (B < 0 || total_q < 0 || max_new < 0 || H < 1 || Hkv < 1 || Dh < 1) return 0;
+  return workspace_of(total_q, H, Dh, dtype, sm_count()).total;
+}
+
+extern "C" int medusa_paged_attn(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                                 const void* v_new, int64_t v_stride, void* k_pages, void* v_pages,
+                                 const medusa_pages_t* pages, const int32_t* rows, const int32_t* q_start, int B,
+                                 int total_q, int max_new, const medusa_tree_t* tree, int H, int Hkv, int Dh,
+                                 float rope_theta, float scale, medusa_dtype dtype, void* out, void* workspace,
+                                 size_t workspace_bytes, int32_t* err, void* stream) {
+  const char* fn = "medusa_paged_attn";
+  if (int rc = check_pages(pages, fn)) return rc;
+  if (int rc = check_pool(k_pages, v_pages, pages->num_pages, pages->page_size, Hkv, Dh, dtype, fn)) return rc;
+  if (tree)
+    if (int rc = check_tree(tree, fn)) return rc;
+  if (B < 0 || B > MEDUSA_MAX_ROWS || (!rows && B > pages->rows) || total_q < 0 || max_new < 0 || max_new > (1 << 24))
+    return fail(MEDUSA_ERR_INVALID, "%s: B=%d total_q=%d max_new=%d", fn, B, total_q, max_new);
+  if (H < Hkv || H % Hkv || H / Hkv > kPagedMaxGroup)
+    return fail(MEDUSA_ERR_UNSUPPORTED, "%s: H=%d Hkv=%d (H a multiple of Hkv, H / Hkv at most %d)", fn, H, Hkv,
+                kPagedMaxGroup);
+  if ((int64_t)total_q * H >= (1ll << 31))
+    return fail(MEDUSA_ERR_UNSUPPORTED, "%s: total_q * H must be below 2^31", fn);
+  if (!(rope_theta > 0.f) || !(scale > 0.f)) return fail(MEDUSA_ERR_INVALID, "%s: rope_theta/scale", fn);
+  if (B == 0 || total_q == 0 || max_new == 0) return MEDUSA_OK;
+  if (!q || !k_new || !v_new || !out || !q_start) return fail(MEDUSA_ERR_INVALID, "%s: NULL tensor", fn);
+  const int es = dtype == MEDUSA_BF16 ? 2 : 4;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new) |
+       reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(workspace)) % 16 ||
+      ((q_stride | k_stride | v_stride) * es) % 16)
+    return fail(MEDUSA_ERR_INVALID, "%s: tensors or strides not 16-byte aligned", fn);
+  if (total_q > 1 && (q_stride < (int64_t)H * Dh || k_stride < (int64_t)Hkv * Dh || v_stride < (int64_t)Hkv * Dh))
+    return fail(MEDUSA_ERR_INVALID, "%s: a token stride is shorter than a token's heads", fn);
+  const int sms = sm_count();
+  const PagedWorkspace w = workspace_of(total_q, H, Dh, dtype, sms);
+  if (!workspace || workspace_bytes < w.total)
+    return fail(MEDUSA_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, w.total);
+  auto* ws = static_cast<uint8_t*>(workspace);
+  PagedAttnArgs a{};
+  a.q = q; a.k_new = k_new; a.v_new = v_new;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.k_pages = k_pages; a.v_pages = v_pages;
+  a.p = pages_dev(pages);
+  a.rows = rows; a.q_start = q_start; a.B = B; a.total_q = total_q; a.max_new = max_new;
+  if (tree) {
+    a.T = tree->T; a.W = tree->W; a.K = tree->K; a.depth = tree->depth; a.anc = tree->anc_mask;
+  }
+  a.H = H; a.Hkv = Hkv; a.g = H / Hkv;
+  for (int j = 0; j < Dh / 2; ++j) {
+    // the fraction of a turn per position; theta < 1 may turn more than once
+    double f = std::pow((double)rope_theta, -2.0 * j / (double)Dh) / 6.283185307179586476925;
+    f -= std::floor(f);
+    a.turns[j] = (uint64_t)std::ldexp(f, 64);
+  }
+  a.qscale = scale * kPagedLog2e;
+  a.out = out;
+  a.q_rot = ws + w.q_rot;
+  a.counters = reinterpret_cast<int*>(ws);
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.err = err;
+  const PagedKernels k{as_stream(stream), sms};
+  a.r_lo = 1;
+  a.r_hi = 0x7fffffff;
+  if (int rc = launch_paged_prep(a, Dh, dtype, k)) return rc;
+  const bool few = (int64_t)max_new * a.g <= 16;
+  return launch_paged_generic(a, Dh, dtype, few, k);
+}

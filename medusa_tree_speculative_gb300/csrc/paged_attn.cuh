@@ -1,0 +1,303 @@
+// Chunk attention over the paged cache: what its kernels share.
+//
+// Work is cut into units (sequence, key head, block of query rows).  The g =
+// H / Hkv query heads of a key head are rows of one matrix: row r of a
+// sequence's key head is token r / g, head r % g, and a block holds whole
+// tokens (RB / g of them), so that one pass over the keys serves all g heads.
+// A unit reads the key tiles its last token sees.  All units' tiles, in the
+// order (sequence, key head, block, tile), form one list, which the grid's
+// CTAs share out evenly: CTA c of G takes tiles [c N / G, (c + 1) N / G).  So
+// ragged batches, one long sequence and a causal triangle are balanced alike,
+// and nothing about the lengths is needed on the host.  A unit that several
+// CTAs share is joined by the last of them to finish (an arrival counter);
+// every partial goes through the workspace and is added in CTA order, whoever
+// adds it, so the result does not depend on timing.
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "paged.cuh"
+
+namespace medusa {
+
+constexpr int kPagedMaxGroup = 64;     // query heads per key head
+constexpr int kPagedCounters = 1024;   // arrival counters of one kernel
+constexpr float kPagedLog2e = 1.4426950408889634f;
+
+struct PagedAttnArgs {
+  const void* q;
+  const void* k_new;
+  const void* v_new;
+  int64_t q_stride, k_stride, v_stride;
+  void* k_pages;
+  void* v_pages;
+  PagesDev p;
+  const int32_t* rows;
+  const int32_t* q_start;
+  int B, total_q, max_new;
+  int T, W, K;  // tree rows (0: causal), mask words per row, depth
+  const int32_t* depth;
+  const uint32_t* anc;
+  int H, Hkv, g;
+  uint64_t turns[64];  // theta^(-2j/Dh) / (2 pi) as a fraction of 2^64
+  float qscale;        // scale * log2(e)
+  void* out;
+  void* q_rot;         // [Hkv][total_q * g][Dh]: rotated queries times qscale
+  int* counters;
+  float* part;         // two partials per CTA: RB rows of Dh sums, then RB (max, sum) pairs
+  int r_lo, r_hi;      // this kernel's sequences: r_lo <= n * g <= r_hi
+  int32_t* err;
+};
+
+// Sequence b: its row, tokens and prefix; false (and an error code, 0 where it
+// merely has no tokens) if it is skipped.
+struct SeqInfo {
+  int row, q0, n, L;
+};
+MDEV bool seq_info(const PagedAttnArgs& a, int b, SeqInfo& s, int& code) {
+  code = 0;
+  s.q0 = a.q_start[b];
+  const int q1 = a.q_start[b + 1];
+  s.row = a.rows ? a.rows[b] : b;
+  s.n = 0;
+  s.L = 0;
+  if (s.q0 < 0 || q1 < s.q0 || q1 > a.total_q || q1 - s.q0 > a.max_new || (a.T && q1 != s.q0 && q1 - s.q0 != a.T)) {
+    code = MEDUSA_DEVERR_LENGTH;
+    return false;
+  }
+  if ((unsigned)s.row >= (unsigned)a.p.rows) {
+    code = MEDUSA_DEVERR_ROW;
+    return false;
+  }
+  s.n = q1 - s.q0;
+  s.L = a.p.length[s.row];
+  const int held = a.p.held[s.row];
+  if (!row_state_ok(a.p, s.L, held)) code = MEDUSA_DEVERR_PAGE;
+  else if ((int64_t)s.L + s.n > (int64_t)held * a.p.page_size) code = MEDUSA_DEVERR_CAPACITY;
+  return code == 0 && s.n > 0;
+}
+
+// Key tiles of block u (tb tokens per block) of a sequence.
+template <int KT>
+MDEV int unit_tiles(const PagedAttnArgs& a, const SeqInfo& s, int tb, int u) {
+  const int seen = a.T ? s.n : min(s.n, (u + 1) * tb);
+  return (s.L + seen + KT - 1) / KT;
+}
+// Sum of unit_tiles over blocks 0 .. u-1, all of them full: sum over i of
+// floor((L + (i + 1) tb + KT - 1) / KT), by Euclid's reduction of the sum of
+// floor((A i + C) / M) (lattice points below a line).
+template <int KT>
+MDEV int64_t tiles_before(const PagedAttnArgs& a, const SeqInfo& s, int tb, int u) {
+  if (u <= 0) return 0;
+  if (a.T) return (int64_t)u * ((s.L + s.n + KT - 1) / KT);
+  uint64_t n = (uint64_t)u, m = KT, x = (uint64_t)tb, c = (uint64_t)s.L + tb + KT - 1;
+  int64_t sum = 0;
+  while (true) {
+    sum += (int64_t)((n - 1) * n / 2 * (x / m));
+    x %= m;
+    sum += (int64_t)(n * (c / m));
+    c %= m;
+    const uint64_t y = x * n + c;
+    if (y < m) break;
+    n = y / m;
+    c = y % m;
+    const uint64_t t = m;
+    m = x;
+    x = t;
+  }
+  return sum;
+}
+// Tiles of one key head of a sequence.
+template <int KT>
+MDEV int64_t seq_tiles(const PagedAttnArgs& a, const SeqInfo& s, int tb) {
+  const int m = (s.n + tb - 1) / tb;
+  return tiles_before<KT>(a, s, tb, m - 1) + unit_tiles<KT>(a, s, tb, m - 1);
+}
+
+// Shared memory for the plan: scratch, used only while it is made, and what
+// stays.
+struct PlanScratch {
+  int owner[MEDUSA_MAX_ROWS];        // cache row -> the first entry that names it
+  int64_t pre[MEDUSA_MAX_ROWS + 1];  // tiles before each sequence
+};
+struct Plan {
+  uint32_t valid[MEDUSA_MAX_ROWS / 32];  // this kernel's sequences
+  int64_t total;                         // tiles in all
+  int64_t warp_sum[33];
+};
+
+// Where in the list a CTA stands: a unit and the tiles of it that are its own.
+struct Segment {
+  SeqInfo s;
+  int b, head, u, m, tiles;  // m blocks; tiles of this unit
+  int t0, t1;
+  int64_t unit_x;            // the unit's first tile in the list
+};
+
+// Build the plan (all NT threads of the CTA); x0, x1: this CTA's tiles.
+template <int NT, int RB, int KT>
+MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& x0, int64_t& x1) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int tb = RB / a.g;
+  if (a.rows) {
+    for (int r = t; r < a.p.rows; r += NT) sc.owner[r] = 0x7fffffff;
+  }
+  for (int w = t; w < MEDUSA_MAX_ROWS / 32; w += NT) pl.valid[w] = 0u;
+  __syncthreads();
+  if (a.rows) {
+    for (int b = t; b < a.B; b += NT) {
+      const int r = a.rows[b];
+      if ((unsigned)r < (unsigned)a.p.rows && a.q_start[b + 1] > a.q_start[b]) atomicMin(&sc.owner[r], b);
+    }
+    __syncthreads();
+  }
+  const int per = (a.B + NT - 1) / NT;
+  int64_t mine = 0;
+  for (int k = 0; k < per; ++k) {
+    const int b = t * per + k;
+    if (b >= a.B) break;
+    SeqInfo s;
+    int code;
+    bool ok = seq_info(a, b, s, code);
+    if (ok && a.rows && sc.owner[s.row] != b) {
+      ok = false;
+      code = MEDUSA_DEVERR_ROW;
+    }
+    if (code && blockIdx.x == 0) set_err(a.err, code);
+    const int64_t r = (int64_t)s.n * a.g;
+    sc.pre[b] = mine;
+    if (ok && r >= a.r_lo && r <= a.r_hi) {
+      atomicOr(&pl.valid[b >> 5], 1u << (b & 31));
+      mine += (int64_t)a.Hkv * seq_tiles<KT>(a, s, tb);
+    }
+  }
+  int64_t x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) pl.warp_sum[warp] = x;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    const int64_t v = pl.warp_sum[w];
+    if (w < warp) before += v;
+    total += v;
+  }
+  before += x - mine;
+  for (int k = 0; k < per; ++k) {
+    const int b = t * per + k;
+    if (b < a.B) sc.pre[b] += before;
+  }
+  if (t == 0) {
+    sc.pre[a.B] = total;
+    pl.total = total;
+  }
+  __syncthreads();
+  const int64_t G = min((int64_t)gridDim.x, total);
+  if ((int64_t)blockIdx.x < G) {
+    x0 = (int64_t)blockIdx.x * total / G;
+    x1 = ((int64_t)blockIdx.x + 1) * total / G;
+  } else {
+    x0 = x1 = 0;
+  }
+}
+
+// The segment of the list that starts at tile x (x < x1).
+template <int RB, int KT>
+MDEV void seek_segment(const PagedAttnArgs& a, const PlanScratch& sc, int64_t x, int64_t x1, Segment& g) {
+  const int tb = RB / a.g;
+  int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before x: it has tiles, or total would be x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sc.pre[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  g.b = lo;
+  int code;
+  seq_info(a, lo, g.s, code);
+  g.m = (g.s.n + tb - 1) / tb;
+  const int64_t each = seq_tiles<KT>(a, g.s, tb);
+  int64_t rest = x - sc.pre[lo];
+  g.head = (int)(rest / each);
+  rest -= (int64_t)g.head * each;
+  int ulo = 0, uhi = g.m - 1;
+  while (ulo < uhi) {
+    const int mid = (ulo + uhi + 1) >> 1;
+    if (tiles_before<KT>(a, g.s, tb, mid) <= rest) ulo = mid; else uhi = mid - 1;
+  }
+  g.u = ulo;
+  rest -= tiles_before<KT>(a, g.s, tb, ulo);
+  g.tiles = unit_tiles<KT>(a, g.s, tb, ulo);
+  g.unit_x = x - rest;
+  g.t0 = (int)rest;
+  g.t1 = (int)min((int64_t)g.tiles, rest + (x1 - x));
+}
+
+// The segment after g (which ended at its unit's end), starting at tile x.
+template <int RB, int KT>
+MDEV void next_segment(const PagedAttnArgs& a, const Plan& pl, int64_t x, int64_t x1, Segment& g) {
+  const int tb = RB / a.g;
+  if (++g.u == g.m) {
+    g.u = 0;
+    if (++g.head == a.Hkv) {
+      g.head = 0;
+      do ++g.b; while (g.b < a.B && !(pl.valid[g.b >> 5] >> (g.b & 31) & 1u));
+      if (g.b >= a.B) {  // not reached: x < x1 <= total
+        g.t0 = g.t1 = 0;
+        return;
+      }
+      int code;
+      seq_info(a, g.b, g.s, code);
+      g.m = (g.s.n + tb - 1) / tb;
+    }
+  }
+  g.tiles = unit_tiles<KT>(a, g.s, tb, g.u);
+  g.unit_x = x;
+  g.t0 = 0;
+  g.t1 = (int)min((int64_t)g.tiles, x1 - x);
+}
+
+// CTA that holds tile x of the list.
+MDEV int cta_of(int64_t x, int64_t total, int64_t G) { return (int)(((x + 1) * G - 1) / total); }
+
+// Who shares the unit of g: its first and last CTA.
+MDEV void unit_shares(const Segment& g, int64_t total, int64_t G, int& first, int& last) {
+  first = cta_of(g.unit_x, total, G);
+  last = cta_of(g.unit_x + g.tiles - 1, total, G);
+}
+// Slot (of two) of CTA c's partial of the unit that starts at unit_x: 0 if it
+// is the CTA's first segment, else 1.
+MDEV int part_slot(int64_t unit_x, int c, int64_t total, int64_t G) {
+  const int64_t x0 = (int64_t)c * total / G;
+  return 2 * c + (x0 >= unit_x ? 0 : 1);
+}
+
+// Whether token i of the sequence sees key x.
+MDEV bool key_seen(const PagedAttnArgs& a, const SeqInfo& s, int i, int x) {
+  if (a.T == 0) return x <= s.L + i;
+  const int node = x - s.L;
+  if (node < 0) return true;
+  return node < a.T && (__ldg(a.anc + (int64_t)i * a.W + (node >> 5)) >> (node & 31) & 1u);
+}
+
+// The page of key x of a row, or -1 (and MEDUSA_DEVERR_PAGE) where the table
+// names none.  x must lie in a held page.
+MDEV int page_of(const PagedAttnArgs& a, const SeqInfo& s, int x) {
+  const int page = a.p.table[(int64_t)s.row * a.p.max_pages + (x >> a.p.shift)];
+  if (page_ok(a.p, page)) return page;
+  set_err(a.err, MEDUSA_DEVERR_PAGE);
+  return -1;
+}
+
+// Host side: launches of the kernels (paged_attn.cu picks).
+struct PagedKernels {
+  cudaStream_t stream;
+  int sms;
+};
+int launch_paged_prep(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, const PagedKernels& k);
+int launch_paged_generic(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, bool few_rows, const PagedKernels& k);
+
+}  // namespace medusa

@@ -16,9 +16,9 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmedusa.so")
 
 MEDUSA_F32, MEDUSA_BF16 = 0, 1
-MAX_T, MAX_K, MAX_S, MAX_B = 512, 8, 16, 16
+MAX_T, MAX_K, MAX_S, MAX_B, MAX_ROWS = 512, 8, 16, 16, 1024
 STATUS = {0: "OK", -1: "INVALID", -2: "UNSUPPORTED", -3: "CAPACITY", -4: "WORKSPACE", -5: "CUDA"}
-DEVERR = {1: "TOKEN", 2: "NODE", 4: "CAPACITY", 8: "LENGTH", 16: "TIMEOUT"}
+DEVERR = {1: "TOKEN", 2: "NODE", 4: "CAPACITY", 8: "LENGTH", 16: "TIMEOUT", 32: "PAGE", 64: "ROW"}
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -36,8 +36,16 @@ class medusa_tree_t(C.Structure):
     ]
 
 
-P, I, F, SZ = C.c_void_p, C.c_int, C.c_float, C.c_size_t
-TREE = C.POINTER(medusa_tree_t)
+class medusa_pages_t(C.Structure):
+    _fields_ = [
+        ("refs", C.c_void_p), ("free_bits", C.c_void_p), ("length", C.c_void_p), ("held", C.c_void_p),
+        ("table", C.c_void_p), ("num_pages", C.c_int32), ("page_size", C.c_int32), ("rows", C.c_int32),
+        ("max_pages", C.c_int32),
+    ]
+
+
+P, I, F, SZ, I64 = C.c_void_p, C.c_int, C.c_float, C.c_size_t, C.c_int64
+TREE, PAGES = C.POINTER(medusa_tree_t), C.POINTER(medusa_pages_t)
 
 _SIGS = {
     "medusa_last_error": (C.c_char_p, []),
@@ -75,6 +83,18 @@ _SIGS = {
     "medusa_standin_embed": (I, [P, I, P, I, I, I, P, P, P]),
     "medusa_heads_logits_topk_workspace_size": (SZ, [I, I, I, I]),
     "medusa_heads_logits_topk": (I, [P, I, P, P, P, I, I, I, I, I, P, P, I, P, SZ, P, P]),
+    "medusa_pages_init": (I, [PAGES, P]),
+    "medusa_pages_free": (I, [PAGES, P, P, P]),
+    "medusa_pages_fork": (I, [PAGES, P, P, I, P, P]),
+    "medusa_pages_reserve": (I, [PAGES, P, P, I, P, P, P, P]),
+    "medusa_pages_commit": (I, [PAGES, P, P, I, I, P, P]),
+    "medusa_pages_compact_workspace_size": (SZ, [I]),
+    "medusa_pages_compact": (I, [PAGES, P, I, P, P, SZ, P, P]),
+    "medusa_pages_copy": (I, [P, P, I, I, I, I, I, P, P, I, P, P]),
+    "medusa_paged_attn_workspace_size": (SZ, [I, I, I, I, I, I, I]),
+    "medusa_paged_attn": (I, [P, I64, P, I64, P, I64, P, P, PAGES, P, P, I, I, I, TREE, I, I, I, F, F, I, P, P, SZ, P,
+                              P]),
+    "medusa_paged_compact": (I, [P, P, PAGES, P, P, P, I, I, I, I, I, I, P, P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -459,3 +479,208 @@ def medusa_accept_stats(stats, groups, logits, tokens, tree: DeviceTree, mode, t
                                     float(temperature), float(eps), float(delta), _ptr(accept_len),
                                     _ptr(accepted_nodes), _ptr(next_root), _ptr(best_node), _ptr(best_logp),
                                     _ptr(err), _stream(stream)), "medusa_accept_stats")
+
+
+# ----------------------------------------------------------- paged cache ---
+
+class Pages:
+    """The bookkeeping of a paged cache (medusa_pages_t): refs [num_pages], free_bits [ceil(num_pages / 32)] (int32
+    view of the words), length [rows], held [rows] and table [rows][max_pages], views of one int32 tensor, `state`,
+    which a caller may clone and copy back to return to an earlier state."""
+
+    def __init__(self, rows: int, max_pages: int, num_pages: int, page_size: int, device="cuda", stream=None):
+        import torch
+
+        self._bind(torch.empty(self.state_size(rows, max_pages, num_pages), dtype=torch.int32, device=device), rows,
+                   max_pages, num_pages, page_size)
+        medusa_pages_init(self, stream)
+
+    @staticmethod
+    def state_size(rows, max_pages, num_pages) -> int:
+        return num_pages + (num_pages + 31) // 32 + 2 * rows + rows * max_pages
+
+    @classmethod
+    def from_state(cls, state, rows: int, max_pages: int, num_pages: int, page_size: int) -> "Pages":
+        """The cache whose arrays lie in `state` (the layout of another Pages' state)."""
+        self = cls.__new__(cls)
+        self._bind(state, rows, max_pages, num_pages, page_size)
+        return self
+
+    def _bind(self, state, rows, max_pages, num_pages, page_size):
+        import torch
+
+        if state.dtype != torch.int32 or not state.is_contiguous() or \
+                state.numel() != self.state_size(rows, max_pages, num_pages):
+            raise ValueError("Pages: the state is a dense int32 tensor of Pages.state_size(rows, max_pages, num_pages)")
+        self.state = state
+        self.refs, self.free_bits, self.length, self.held, table = torch.split(
+            state, [num_pages, (num_pages + 31) // 32, rows, rows, rows * max_pages])
+        self.table = table.view(rows, max_pages)
+        self.rows, self.max_pages, self.num_pages, self.page_size = rows, max_pages, num_pages, page_size
+        self.device = state.device
+        self.struct = medusa_pages_t(self.refs.data_ptr(), self.free_bits.data_ptr(), self.length.data_ptr(),
+                                     self.held.data_ptr(), self.table.data_ptr(), num_pages, page_size, rows, max_pages)
+        self.ref = C.byref(self.struct)
+
+
+def _dense(t, name, shape=None, dtype=None, pages=None):
+    """Pointer of a dense tensor (None: NULL), refused if its shape, dtype or device is another than the call's."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: libmedusa takes dense row-major tensors")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+    if pages is not None and t.device != pages.device:
+        raise ValueError(f"{name}: on {t.device}, the cache is on {pages.device}")
+    return t.data_ptr()
+
+
+def _stream_on(stream, device):
+    """The stream to launch on, refused unless `device` (a CUDA device) is the current one."""
+    import torch
+
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"libmedusa works on the current CUDA device; these tensors are on {device}")
+    return _stream(stream)
+
+
+def _i32():
+    import torch
+
+    return torch.int32
+
+
+def _pool(k_pages, v_pages, pages=None):
+    """(num_pages, Hkv, page_size, Dh, dtype code) of a layer's pools."""
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+        raise ValueError("k_pages and v_pages: two [num_pages][Hkv][page_size][Dh] tensors of one type")
+    n, Hkv, ps, Dh = k_pages.shape
+    if pages is not None and (n != pages.num_pages or ps != pages.page_size):
+        raise ValueError(f"pools of {n} pages of {ps} tokens, the cache has {pages.num_pages} of {pages.page_size}")
+    return n, Hkv, ps, Dh, _dtype(k_pages)
+
+
+def medusa_pages_init(pages: Pages, stream=None):
+    """Every page free, every row empty."""
+    _check(_lib.medusa_pages_init(pages.ref, _stream_on(stream, pages.device)), "medusa_pages_init")
+
+
+def medusa_pages_free(pages: Pages, keep_len, err=None, stream=None):
+    """Rows with keep_len[r] >= 0 keep their first keep_len[r] tokens; keep_len [rows] int32."""
+    i32 = _i32()
+    _check(_lib.medusa_pages_free(pages.ref, _dense(keep_len, "keep_len", (pages.rows,), i32, pages),
+                                  _dense(err, "err", None, i32, pages), _stream_on(stream, pages.device)),
+           "medusa_pages_free")
+
+
+def medusa_pages_fork(pages: Pages, src, dst, err=None, stream=None):
+    """Row dst[i] (empty) becomes a second holder of row src[i]'s tokens; src, dst [n] int32."""
+    n, i32 = src.shape[0], _i32()
+    _check(_lib.medusa_pages_fork(pages.ref, _dense(src, "src", (n,), i32, pages),
+                                  _dense(dst, "dst", (n,), i32, pages), n, _dense(err, "err", None, i32, pages),
+                                  _stream_on(stream, pages.device)), "medusa_pages_fork")
+
+
+def medusa_pages_reserve(pages: Pages, n_new, copies, n_copies, granted=None, err=None, stream=None):
+    """Room for n_new[r] more tokens per row; copies [>= rows][4] and n_copies [1] (int32) for medusa_pages_copy."""
+    i32 = _i32()
+    _check(_lib.medusa_pages_reserve(pages.ref, _dense(n_new, "n_new", (pages.rows,), i32, pages),
+                                     _dense(copies, "copies", (copies.shape[0], 4), i32, pages), copies.shape[0],
+                                     _dense(n_copies, "n_copies", (1,), i32, pages),
+                                     _dense(granted, "granted", (pages.rows,), i32, pages),
+                                     _dense(err, "err", None, i32, pages), _stream_on(stream, pages.device)),
+           "medusa_pages_reserve")
+
+
+def medusa_pages_commit(pages: Pages, rows, n_new, bias: int = 0, err=None, stream=None):
+    """length[rows[b]] += n_new[b] + bias (rows None: row b)."""
+    B, i32 = n_new.shape[0], _i32()
+    _check(_lib.medusa_pages_commit(pages.ref, _dense(rows, "rows", (B,), i32, pages),
+                                    _dense(n_new, "n_new", (B,), i32, pages), int(bias), B,
+                                    _dense(err, "err", None, i32, pages), _stream_on(stream, pages.device)),
+           "medusa_pages_commit")
+
+
+def medusa_pages_compact_workspace_size(num_pages: int) -> int:
+    return int(_lib.medusa_pages_compact_workspace_size(num_pages))
+
+
+def medusa_pages_compact(pages: Pages, copies, n_copies, workspace, err=None, stream=None):
+    """The live pages to the front of the pool; copies [max_copies][4] and n_copies [1] for medusa_pages_copy."""
+    i32 = _i32()
+    _check(_lib.medusa_pages_compact(pages.ref, _dense(copies, "copies", (copies.shape[0], 4), i32, pages),
+                                     copies.shape[0], _dense(n_copies, "n_copies", (1,), i32, pages),
+                                     _dense(workspace, "workspace", None, None, pages),
+                                     workspace.numel() * workspace.element_size(),
+                                     _dense(err, "err", None, i32, pages), _stream_on(stream, pages.device)),
+           "medusa_pages_compact")
+
+
+def medusa_pages_copy(k_pages, v_pages, copies, n_copies, err=None, stream=None):
+    """Carry out a list of page copies in one layer's pools [num_pages][Hkv][page_size][Dh]."""
+    n, Hkv, ps, Dh, dt = _pool(k_pages, v_pages)
+    i32 = _i32()
+    _check(_lib.medusa_pages_copy(_dense(k_pages, "k_pages"), _dense(v_pages, "v_pages", None, None, k_pages), n, ps,
+                                  Hkv, Dh, dt, _dense(copies, "copies", (copies.shape[0], 4), i32, k_pages),
+                                  _dense(n_copies, "n_copies", (1,), i32, k_pages), copies.shape[0],
+                                  _dense(err, "err", None, i32, k_pages), _stream_on(stream, k_pages.device)),
+           "medusa_pages_copy")
+
+
+def medusa_paged_attn_workspace_size(B, total_q, max_new, H, Hkv, Dh, dtype) -> int:
+    """Bytes for these sizes; dtype: torch.bfloat16 or torch.float32.  Zero-fill the workspace once."""
+    import torch
+
+    return int(_lib.medusa_paged_attn_workspace_size(B, total_q, max_new, H, Hkv, Dh,
+                                                     MEDUSA_BF16 if dtype == torch.bfloat16 else MEDUSA_F32))
+
+
+def _heads(t, name, heads, Dh, total, dtype, pages):
+    """Pointer and token stride of [total][heads][Dh], whose tokens may lie any distance apart."""
+    if t.shape != (total, heads, Dh):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(total, heads, Dh)}")
+    st = t.stride()
+    if total and (st[2] != 1 or (heads > 1 and st[1] != Dh)):
+        raise ValueError(f"{name}: a token's heads must lie side by side (strides {st})")
+    if t.dtype != dtype or t.device != pages.device:
+        raise TypeError(f"{name}: {t.dtype} on {t.device}, the pools are {dtype} on {pages.device}")
+    return t.data_ptr(), st[0]
+
+
+def medusa_paged_attn(q, k_new, v_new, k_pages, v_pages, pages: Pages, rows, q_start, max_new: int, tree, rope_theta,
+                      scale, out, workspace, err=None, stream=None):
+    """A chunk of new tokens per sequence over the paged cache: q [total][H][Dh], k_new, v_new [total][Hkv][Dh]
+    (tokens may be strided), q_start [B+1], rows [B] or None, tree a DeviceTree or None (causal), out
+    [total][H][Dh]."""
+    _, Hkv, _, Dh, dt = _pool(k_pages, v_pages, pages)
+    total, H = q.shape[0], q.shape[1]
+    B = q_start.shape[0] - 1
+    ty, i32 = k_pages.dtype, _i32()
+    qp, qs = _heads(q, "q", H, Dh, total, ty, pages)
+    kp, ks = _heads(k_new, "k_new", Hkv, Dh, total, ty, pages)
+    vp, vs = _heads(v_new, "v_new", Hkv, Dh, total, ty, pages)
+    _check(_lib.medusa_paged_attn(qp, qs, kp, ks, vp, vs, _dense(k_pages, "k_pages", None, None, pages),
+                                  _dense(v_pages, "v_pages", None, None, pages), pages.ref,
+                                  _dense(rows, "rows", (B,), i32, pages), _dense(q_start, "q_start", None, i32, pages),
+                                  B, total, max_new, None if tree is None else tree.ref, H, Hkv, Dh, rope_theta, scale,
+                                  dt, _dense(out, "out", (total, H, Dh), ty, pages),
+                                  _dense(workspace, "workspace", None, None, pages),
+                                  workspace.numel() * workspace.element_size(), _dense(err, "err", None, i32, pages),
+                                  _stream_on(stream, pages.device)), "medusa_paged_attn")
+
+
+def medusa_paged_compact(k_pages, v_pages, pages: Pages, rows, accepted_nodes, accept_len, T: int, err=None,
+                         stream=None):
+    """The accepted path's keys and values into place inside the rows' pages, one layer; lengths stay."""
+    _, Hkv, _, Dh, dt = _pool(k_pages, v_pages, pages)
+    (B, Kp), i32 = accepted_nodes.shape, _i32()
+    _check(_lib.medusa_paged_compact(_dense(k_pages, "k_pages", None, None, pages),
+                                     _dense(v_pages, "v_pages", None, None, pages), pages.ref,
+                                     _dense(rows, "rows", (B,), i32, pages),
+                                     _dense(accepted_nodes, "accepted_nodes", None, i32, pages),
+                                     _dense(accept_len, "accept_len", (B,), i32, pages), B, Hkv, Dh, Kp - 1, T, dt,
+                                     _dense(err, "err", None, i32, pages), _stream_on(stream, pages.device)),
+           "medusa_paged_compact")
