@@ -1,6 +1,7 @@
 // Chunk attention over the paged cache: the call, the rotation and append of a
 // chunk, and the kernels on the CUDA cores.
 #include <cmath>
+#include <mutex>
 
 #include "paged_attn.cuh"
 
@@ -380,7 +381,36 @@ PagedWorkspace workspace_of(int total_q, int H, int Dh, medusa_dtype dtype, int 
   return w;
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_fn() {
+  static EncodeTiled fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) ==
+            cudaSuccess &&
+        qr == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiled>(p);
+  });
+  return fn;
+}
+
 }  // namespace
+
+bool make_pool_map(CUtensorMap* m, const void* pool, const PagedAttnArgs& a, int Dh, int box) {
+  EncodeTiled enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)Dh, (cuuint64_t)a.p.num_pages * a.Hkv * a.p.page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)Dh * 2};
+  const cuuint32_t boxes[2] = {64, (cuuint32_t)box};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides, boxes, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 int launch_paged_prep(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, const PagedKernels& k) {
   const dim3 grid((a.total_q + kPrepTokens - 1) / kPrepTokens);
@@ -466,6 +496,7 @@ extern "C" int medusa_paged_attn(const void* q, int64_t q_stride, const void* k_
   const PagedKernels k{as_stream(stream), sms};
   a.r_lo = 1;
   a.r_hi = 0x7fffffff;
+  if (dtype == MEDUSA_BF16 && (int64_t)max_new * a.g <= 16) return launch_paged_decode(a, Dh, k);
   if (int rc = launch_paged_prep(a, Dh, dtype, k)) return rc;
   const bool few = (int64_t)max_new * a.g <= 16;
   return launch_paged_generic(a, Dh, dtype, few, k);

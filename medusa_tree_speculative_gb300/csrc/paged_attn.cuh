@@ -16,9 +16,12 @@
 
 #include <stdint.h>
 
+#include <cuda.h>
+
 #include "common.cuh"
 #include "internal.h"
 #include "paged.cuh"
+#include "sm100.cuh"
 
 namespace medusa {
 
@@ -292,12 +295,29 @@ MDEV int page_of(const PagedAttnArgs& a, const SeqInfo& s, int x) {
   return -1;
 }
 
+// Wait for a barrier's phase.  After kSpinLimit polls, or once another thread
+// of the CTA has given up, it returns all the same: the caller goes on, through
+// every barrier as ever, on whatever data there are, and the kernel's end
+// reports MEDUSA_DEVERR_TIMEOUT.
+MDEV void paged_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  for (uint32_t i = 0; i < sm100::kSpinLimit; ++i) {
+    if (sm100::mbar_try_wait(bar, parity)) return;
+    if ((i & 63) == 63 && *abort_flag) return;
+  }
+  *abort_flag = 1;
+}
+
 // Host side: launches of the kernels (paged_attn.cu picks).
 struct PagedKernels {
   cudaStream_t stream;
   int sms;
 };
 int launch_paged_prep(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, const PagedKernels& k);
+// A pool as lines of Dh bf16, in boxes of `box` lines x 64 values, 128-byte
+// swizzle; lines past the pool read zeros.
+bool make_pool_map(CUtensorMap* m, const void* pool, const PagedAttnArgs& a, int Dh, int box);
+size_t paged_decode_part_bytes(int Dh, int sms);
+int launch_paged_decode(const PagedAttnArgs& a, int Dh, const PagedKernels& k);
 int launch_paged_generic(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, bool few_rows, const PagedKernels& k);
 
 }  // namespace medusa
