@@ -1,5 +1,5 @@
 // Chunk attention over the paged cache: the call, the rotation and append of a
-// chunk, and the kernels on the CUDA cores.
+// chunk, and the float32 kernels.
 #include <cmath>
 #include <mutex>
 
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_c
   }
 }
 
-// -------------------------------------------------- CUDA-core kernel --
+// ------------------------------------------------------ float32 kernel --
 // S = Q K^T and O += P V on the CUDA cores: 256 threads as 16 x 16, thread
 // (ty, tx) with rows ty + 16 a of the block, keys tx + 16 b of the tile and,
 // for O, columns tx * 4 + 64 c.  A row's sixteen threads are half a warp, so
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_c
 // value tile loads while S is computed and the next key tile while O is.
 constexpr int kGenThreads = 256;
 
-template <typename T, int DH, int RB, int KT>
+template <int DH, int RB, int KT>
 struct Gen {
   static constexpr int TM = RB / 16, TN = KT / 16, CC = DH / 64;
   static constexpr int kQ = RB * (DH + 4), kK = KT * (DH + 4), kV = KT * DH, kP = RB * (KT + 4);
@@ -135,9 +135,9 @@ struct Gen {
   static constexpr int part_floats = RB * DH + 2 * RB;
 };
 
-template <typename T, int DH, int RB, int KT>
+template <int DH, int RB, int KT>
 __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid_constant__ PagedAttnArgs a) {
-  using G = Gen<T, DH, RB, KT>;
+  using G = Gen<DH, RB, KT>;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;                  // [RB][DH + 4]
   float* Ks = Qs + G::kQ;          // [KT][DH + 4]
@@ -159,30 +159,23 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
     const int nkeys = s.L + s.n, tok0 = sg.u * tb, live = min(tb, s.n - tok0) * a.g;
     // one tile of keys or values, zeros where there is none
     auto load = [&](const void* pool, float* dst, int stride, int t) {
-      constexpr int kVec = 16 / sizeof(T), kRow = DH / kVec;
+      constexpr int kRow = DH / 4;
       for (int e = tid; e < KT * kRow; e += kGenThreads) {
         const int key = t * KT + e / kRow, c = e % kRow;
-        const T* src = static_cast<const T*>(pool);
+        const float* src = static_cast<const float*>(pool);
         bool ok = key < nkeys;
         if (ok) {
           const int page = page_of(a, s, key);
           ok = page >= 0;
-          if (ok) src += page_line(a.p, page, a.Hkv, sg.head, key & (a.p.page_size - 1)) * DH + c * kVec;
+          if (ok) src += page_line(a.p, page, a.Hkv, sg.head, key & (a.p.page_size - 1)) * DH + c * 4;
         }
-        float* d = dst + (e / kRow) * stride + c * kVec;
-        if constexpr (sizeof(T) == 4) {
-          cp_async16(smem_u32(d), src, ok ? 16 : 0);
-        } else {
-          float f[8] = {};
-          if (ok) load8(src, f);
-          store8(d, f);
-        }
+        cp_async16(smem_u32(dst + (e / kRow) * stride + c * 4), src, ok ? 16 : 0);
       }
       cp_async_commit();
     };
     __syncthreads();  // the previous segment's tiles are read
     {
-      const T* qr = static_cast<const T*>(a.q_rot) +
+      const float* qr = static_cast<const float*>(a.q_rot) +
                     ((int64_t)sg.head * a.total_q + s.q0 + tok0) * a.g * (int64_t)DH;
       for (int e = tid; e < RB * (DH / 8); e += kGenThreads) {
         const int r = e / (DH / 8), c = e % (DH / 8);
@@ -289,12 +282,12 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
       const int r = ty + 16 * i;
       if (r >= live) return;
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      T* dst = static_cast<T*>(a.out) +
+      float* dst = static_cast<float*>(a.out) +
                ((int64_t)(s.q0 + tok0 + r / a.g) * a.H + (int64_t)sg.head * a.g + r % a.g) * DH;
 #pragma unroll
       for (int c = 0; c < G::CC; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dst[tx * 4 + 64 * c + j] = from_f32<T>(v[c * 4 + j] * inv);
+        *reinterpret_cast<float4*>(dst + tx * 4 + 64 * c) =
+            make_float4(v[c * 4] * inv, v[c * 4 + 1] * inv, v[c * 4 + 2] * inv, v[c * 4 + 3] * inv);
     };
     if (sg.t0 == 0 && sg.t1 == sg.tiles) {
 #pragma unroll
@@ -351,33 +344,31 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
   }
 }
 
-template <typename T, int DH, int RB, int KT>
+template <int DH, int RB, int KT>
 int run_generic(const PagedAttnArgs& a, const PagedKernels& k) {
-  using G = Gen<T, DH, RB, KT>;
-  auto* fn = paged_generic_kernel<T, DH, RB, KT>;
+  using G = Gen<DH, RB, KT>;
+  auto* fn = paged_generic_kernel<DH, RB, KT>;
   cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::smem);
   launch_kernel(fn, dim3(k.sms * 2), dim3(kGenThreads), G::smem, k.stream, a);
   return check_launch("medusa_paged_attn");
 }
 
-template <typename T>
-int run_generic_t(const PagedAttnArgs& a, int Dh, bool few, const PagedKernels& k) {
-  if (few) return Dh == 64 ? run_generic<T, 64, 16, 64>(a, k) : run_generic<T, 128, 16, 64>(a, k);
-  return Dh == 64 ? run_generic<T, 64, 64, 32>(a, k) : run_generic<T, 128, 64, 32>(a, k);
-}
+size_t generic_part_bytes(int RB, int Dh, int sms) { return (size_t)(sms * 2) * 2 * (RB * Dh + 2 * RB) * 4; }
 
 // The workspace: both kernels' counters first, at the same place for every
 // size, then the rotated queries, then the partials.
 struct PagedWorkspace {
-  size_t q_rot, part, total;
+  size_t q_rot, part_few, part_many, total;
 };
 constexpr size_t kCounterBytes = 2 * kPagedCounters * 4;
 
 PagedWorkspace workspace_of(int total_q, int H, int Dh, medusa_dtype dtype, int sms) {
   PagedWorkspace w;
+  const bool bf16 = dtype == MEDUSA_BF16;
   w.q_rot = kCounterBytes;
-  w.part = align_up(w.q_rot + (size_t)total_q * H * Dh * (dtype == MEDUSA_BF16 ? 2 : 4), 256);
-  w.total = align_up(w.part + (size_t)(sms * 2) * 2 * (64 * Dh + 2 * 64) * 4, 256);
+  w.part_few = align_up(w.q_rot + (size_t)total_q * H * Dh * (bf16 ? 2 : 4), 256);
+  w.part_many = align_up(w.part_few + (bf16 ? paged_decode_part_bytes(Dh, sms) : generic_part_bytes(16, Dh, sms)), 256);
+  w.total = align_up(w.part_many + (bf16 ? paged_chunk_part_bytes(Dh, sms) : generic_part_bytes(64, Dh, sms)), 256);
   return w;
 }
 
@@ -400,14 +391,14 @@ EncodeTiled encode_fn() {
 
 }  // namespace
 
-bool make_pool_map(CUtensorMap* m, const void* pool, const PagedAttnArgs& a, int Dh, int box) {
+bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows, int Dh, int box) {
   EncodeTiled enc = encode_fn();
   if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)Dh, (cuuint64_t)a.p.num_pages * a.Hkv * a.p.page_size};
+  const cuuint64_t dims[2] = {(cuuint64_t)Dh, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)Dh * 2};
   const cuuint32_t boxes[2] = {64, (cuuint32_t)box};
   const cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides, boxes, estr,
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -424,8 +415,9 @@ int launch_paged_prep(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, const 
   return check_launch("medusa_paged_attn");
 }
 
-int launch_paged_generic(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, bool few_rows, const PagedKernels& k) {
-  return dtype == MEDUSA_BF16 ? run_generic_t<uint16_t>(a, Dh, few_rows, k) : run_generic_t<float>(a, Dh, few_rows, k);
+int launch_paged_generic(const PagedAttnArgs& a, int Dh, bool few_rows, const PagedKernels& k) {
+  if (few_rows) return Dh == 64 ? run_generic<64, 16, 64>(a, k) : run_generic<128, 16, 64>(a, k);
+  return Dh == 64 ? run_generic<64, 64, 32>(a, k) : run_generic<128, 64, 32>(a, k);
 }
 
 }  // namespace medusa
@@ -490,14 +482,31 @@ extern "C" int medusa_paged_attn(const void* q, int64_t q_stride, const void* k_
   a.qscale = scale * kPagedLog2e;
   a.out = out;
   a.q_rot = ws + w.q_rot;
-  a.counters = reinterpret_cast<int*>(ws);
-  a.part = reinterpret_cast<float*>(ws + w.part);
   a.err = err;
   const PagedKernels k{as_stream(stream), sms};
-  a.r_lo = 1;
-  a.r_hi = 0x7fffffff;
-  if (dtype == MEDUSA_BF16 && (int64_t)max_new * a.g <= 16) return launch_paged_decode(a, Dh, k);
-  if (int rc = launch_paged_prep(a, Dh, dtype, k)) return rc;
-  const bool few = (int64_t)max_new * a.g <= 16;
-  return launch_paged_generic(a, Dh, dtype, few, k);
+  // Sequences of up to 16 rows per key head, and the others: a launch for each
+  // kind that the call may hold.
+  const bool bf16 = dtype == MEDUSA_BF16;
+  PagedAttnArgs few = a, many = a;
+  few.counters = reinterpret_cast<int*>(ws);
+  few.part = reinterpret_cast<float*>(ws + w.part_few);
+  few.r_lo = 1;
+  few.r_hi = kFewRows;
+  many.counters = few.counters + kPagedCounters;
+  many.part = reinterpret_cast<float*>(ws + w.part_many);
+  many.r_lo = kFewRows + 1;
+  many.r_hi = 0x7fffffff;
+  const bool any_many = (int64_t)max_new * a.g > kFewRows;
+  const bool any_few = a.g <= kFewRows && !(tree && any_many);
+  if (!bf16) {
+    a.r_lo = 1;
+    a.r_hi = 0x7fffffff;
+    if (int rc = launch_paged_prep(a, Dh, dtype, k)) return rc;
+  }
+  if (any_few)
+    if (int rc = bf16 ? launch_paged_decode(few, Dh, k) : launch_paged_generic(few, Dh, true, k)) return rc;
+  if (!any_many) return MEDUSA_OK;
+  if (bf16)
+    if (int rc = launch_paged_prep(many, Dh, dtype, k)) return rc;
+  return bf16 ? launch_paged_chunk(many, Dh, k) : launch_paged_generic(many, Dh, false, k);
 }

@@ -26,6 +26,7 @@
 namespace medusa {
 
 constexpr int kPagedMaxGroup = 64;     // query heads per key head
+constexpr int kFewRows = 16;           // rows (tokens x heads of a key head) of the kernels for few rows
 constexpr int kPagedCounters = 1024;   // arrival counters of one kernel
 constexpr float kPagedLog2e = 1.4426950408889634f;
 
@@ -313,11 +314,16 @@ struct PagedKernels {
   int sms;
 };
 int launch_paged_prep(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, const PagedKernels& k);
-// A pool as lines of Dh bf16, in boxes of `box` lines x 64 values, 128-byte
-// swizzle; lines past the pool read zeros.
-bool make_pool_map(CUtensorMap* m, const void* pool, const PagedAttnArgs& a, int Dh, int box);
+// Rows of Dh bf16 (a pool's lines) in boxes of `box` rows x 64 values, 128-byte
+// swizzle; rows past the last read zeros.
+bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows, int Dh, int box);
+inline bool make_pool_map(CUtensorMap* m, const void* pool, const PagedAttnArgs& a, int Dh, int box) {
+  return make_rows_map(m, pool, (int64_t)a.p.num_pages * a.Hkv * a.p.page_size, Dh, box);
+}
 size_t paged_decode_part_bytes(int Dh, int sms);
 int launch_paged_decode(const PagedAttnArgs& a, int Dh, const PagedKernels& k);
-int launch_paged_generic(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, bool few_rows, const PagedKernels& k);
+size_t paged_chunk_part_bytes(int Dh, int sms);
+int launch_paged_chunk(const PagedAttnArgs& a, int Dh, const PagedKernels& k);
+int launch_paged_generic(const PagedAttnArgs& a, int Dh, bool few_rows, const PagedKernels& k);
 
 }  // namespace medusa
