@@ -40,6 +40,22 @@ int sm_count() {
   return n;
 }
 
+int prepare_kernel(const void* kernel, size_t smem, int min_regs, std::atomic<uint64_t>* done, const char* what) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return check_launch(what);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done->load(std::memory_order_relaxed) & bit) return MEDUSA_OK;
+  cudaFuncAttributes attr = {};
+  if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return check_launch(what);
+  if (attr.numRegs < min_regs)
+    return fail(MEDUSA_ERR_CUDA, "%s: the kernel was built with %d registers a thread, it needs %d", what, attr.numRegs,
+                min_regs);
+  done->fetch_or(bit, std::memory_order_relaxed);
+  return MEDUSA_OK;
+}
+
 int check_tree(const medusa_tree_t* t, const char* what) {
   if (!t) return fail(MEDUSA_ERR_INVALID, "%s: tree is NULL", what);
   if (t->T < 1 || t->T > MEDUSA_MAX_T)

@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "medusa.h"
@@ -38,6 +39,11 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
   cfg.stream = s;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
+// Opt a kernel in to `smem` bytes of shared memory, once per device (`done`: a
+// static of the caller's, a bit per device).  Returns the kernel's attributes'
+// status, MEDUSA_OK or MEDUSA_ERR_CUDA, and with min_regs > 0 checks that it
+// was built with at least that many registers a thread.
+int prepare_kernel(const void* kernel, size_t smem, int min_regs, std::atomic<uint64_t>* done, const char* what);
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 }  // namespace medusa

@@ -51,7 +51,6 @@ struct PagedAttnArgs {
   void* q_rot;         // [Hkv][total_q * g][Dh]: rotated queries times qscale
   int* counters;
   float* part;         // two partials per CTA: RB rows of Dh sums, then RB (max, sum) pairs
-  int r_lo, r_hi;      // this kernel's sequences: r_lo <= n * g <= r_hi
   int32_t* err;
 };
 
@@ -127,7 +126,7 @@ struct PlanScratch {
   int64_t pre[MEDUSA_MAX_ROWS + 1];  // tiles before each sequence
 };
 struct Plan {
-  uint32_t valid[MEDUSA_MAX_ROWS / 32];  // this kernel's sequences
+  uint32_t valid[MEDUSA_MAX_ROWS / 32];  // the sequences that are not skipped
   int64_t total;                         // tiles in all
   int64_t warp_sum[33];
 };
@@ -170,9 +169,8 @@ MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& 
       code = MEDUSA_DEVERR_ROW;
     }
     if (code && blockIdx.x == 0) set_err(a.err, code);
-    const int64_t r = (int64_t)s.n * a.g;
     sc.pre[b] = mine;
-    if (ok && r >= a.r_lo && r <= a.r_hi) {
+    if (ok) {
       atomicOr(&pl.valid[b >> 5], 1u << (b & 31));
       mine += (int64_t)a.Hkv * seq_tiles<KT>(a, s, tb);
     }

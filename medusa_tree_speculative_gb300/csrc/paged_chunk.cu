@@ -569,11 +569,10 @@ int run(const PagedAttnArgs& a, const PagedKernels& k) {
       !make_pool_map(&tmK, a.k_pages, a, DH, box) || !make_pool_map(&tmV, a.v_pages, a, DH, box))
     return fail(MEDUSA_ERR_CUDA, "medusa_paged_attn: cuTensorMapEncodeTiled failed");
   auto* fn = paged_chunk_kernel<DH>;
-  cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<DH>::smem);
-  // the registers' redistribution waits for ever if the block has fewer to give
-  cudaFuncAttributes attr;
-  if (cudaFuncGetAttributes(&attr, fn) != cudaSuccess || attr.numRegs < kLaunchRegs)
-    return fail(MEDUSA_ERR_CUDA, "medusa_paged_attn: the kernel was built with %d registers a thread", attr.numRegs);
+  static std::atomic<uint64_t> done{0};
+  // the registers' redistribution would wait for ever if the block had fewer to give
+  if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), Cfg<DH>::smem, kLaunchRegs, &done, "medusa_paged_attn"))
+    return rc;
   launch_kernel(fn, dim3(k.sms), dim3(kThreads), Cfg<DH>::smem, k.stream, tmQ, tmK, tmV, a);
   return check_launch("medusa_paged_attn");
 }

@@ -20,7 +20,7 @@
 // one with that tile of that key head) rotates and appends them: no separate
 // launch.
 // P, unlike the queries, is rounded once to bf16 (a relative 2^-8 a weight,
-// independent from key to key) unless kSplitP.
+// independent from key to key).
 #include "paged_attn.cuh"
 #include "sm100.cuh"
 
@@ -439,7 +439,8 @@ int run(const PagedAttnArgs& a, const PagedKernels& k) {
   if (!make_pool_map(&tmK, a.k_pages, a, DH, box) || !make_pool_map(&tmV, a.v_pages, a, DH, box))
     return fail(MEDUSA_ERR_CUDA, "medusa_paged_attn: cuTensorMapEncodeTiled failed");
   auto* fn = paged_decode_kernel<DH>;
-  cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<DH>::smem);
+  static std::atomic<uint64_t> done{0};
+  if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), Cfg<DH>::smem, 0, &done, "medusa_paged_attn")) return rc;
   launch_kernel(fn, dim3(k.sms), dim3(kThreads), Cfg<DH>::smem, k.stream, tmK, tmV, a);
   return check_launch("medusa_paged_attn");
 }

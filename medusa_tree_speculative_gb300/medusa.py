@@ -482,6 +482,8 @@ def medusa_accept_stats(stats, groups, logits, tokens, tree: DeviceTree, mode, t
 
 
 # ----------------------------------------------------------- paged cache ---
+# A decode step makes several of these calls per layer, each of a few
+# microseconds on the GPU: the checks below are few and cheap on purpose.
 
 class Pages:
     """The bookkeeping of a paged cache (medusa_pages_t): refs [num_pages], free_bits [ceil(num_pages / 32)] (int32
@@ -518,90 +520,110 @@ class Pages:
         self.table = table.view(rows, max_pages)
         self.rows, self.max_pages, self.num_pages, self.page_size = rows, max_pages, num_pages, page_size
         self.device = state.device
+        self.index = state.get_device()  # -1: not on a GPU
         self.struct = medusa_pages_t(self.refs.data_ptr(), self.free_bits.data_ptr(), self.length.data_ptr(),
                                      self.held.data_ptr(), self.table.data_ptr(), num_pages, page_size, rows, max_pages)
         self.ref = C.byref(self.struct)
 
 
-def _dense(t, name, shape=None, dtype=None, pages=None):
-    """Pointer of a dense tensor (None: NULL), refused if its shape, dtype or device is another than the call's."""
+class _Torch:
+    """torch's int32 and the two queries that a launch needs, looked up once."""
+
+    int32 = None
+
+    @classmethod
+    def load(cls):
+        import torch
+
+        cls.bf16, cls.f32 = torch.bfloat16, torch.float32
+        cls.current_device = staticmethod(torch.cuda.current_device)
+        cls.raw_stream = staticmethod(getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                                      (lambda index: torch.cuda.current_stream(index).cuda_stream))
+        cls.int32 = torch.int32
+
+
+def _launch_on(stream, index):
+    """The stream to launch on; device `index`, where the tensors are, has to be the current one."""
+    if _Torch.int32 is None:
+        _Torch.load()
+    if index < 0 or index != _Torch.current_device():
+        raise ValueError(f"libmedusa works on the current CUDA device; these tensors are on "
+                         f"{'the CPU' if index < 0 else 'cuda:%d' % index}")
+    if stream is None:
+        return _Torch.raw_stream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(t, name, index, n=None, dtype=None):
+    """Pointer of a dense tensor of n elements (None: any number) of dtype (None: any) on device `index`."""
     if t is None:
         return None
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: libmedusa takes dense row-major tensors")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
-    if pages is not None and t.device != pages.device:
-        raise ValueError(f"{name}: on {t.device}, the cache is on {pages.device}")
-    return t.data_ptr()
+    if t.get_device() == index and t.is_contiguous() and (n is None or t.numel() == n) and \
+            (dtype is None or t.dtype is dtype):
+        return t.data_ptr()
+    raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}; expected a dense "
+                     f"{dtype or ''} tensor{'' if n is None else ' of %d elements' % n} on the cache's device")
 
 
-def _stream_on(stream, device):
-    """The stream to launch on, refused unless `device` (a CUDA device) is the current one."""
-    import torch
-
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"libmedusa works on the current CUDA device; these tensors are on {device}")
-    return _stream(stream)
+def _ints(t, name, index, n=None):
+    if _Torch.int32 is None:
+        _Torch.load()
+    return _on(t, name, index, n, _Torch.int32)
 
 
-def _i32():
-    import torch
+def _lines(copies):
+    if copies.dim() != 2 or copies.shape[1] != 4:
+        raise ValueError(f"copies: shape {tuple(copies.shape)}, expected [lines][4]")
+    return copies.shape[0]
 
-    return torch.int32
 
-
-def _pool(k_pages, v_pages, pages=None):
-    """(num_pages, Hkv, page_size, Dh, dtype code) of a layer's pools."""
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+def _pool(k_pages, v_pages, index, pages=None):
+    """Pointers, sizes (num_pages, Hkv, page_size, Dh) and dtype code of a layer's pools."""
+    if _Torch.int32 is None:
+        _Torch.load()
+    shape, dtype = k_pages.shape, k_pages.dtype
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages: two [num_pages][Hkv][page_size][Dh] tensors of one type")
-    n, Hkv, ps, Dh = k_pages.shape
-    if pages is not None and (n != pages.num_pages or ps != pages.page_size):
-        raise ValueError(f"pools of {n} pages of {ps} tokens, the cache has {pages.num_pages} of {pages.page_size}")
-    return n, Hkv, ps, Dh, _dtype(k_pages)
+    if pages is not None and (shape[0] != pages.num_pages or shape[2] != pages.page_size):
+        raise ValueError(f"pools of {shape[0]} pages of {shape[2]} tokens, the cache has {pages.num_pages} of "
+                         f"{pages.page_size}")
+    code = MEDUSA_BF16 if dtype is _Torch.bf16 else MEDUSA_F32 if dtype is _Torch.f32 else _dtype(k_pages)
+    return _on(k_pages, "k_pages", index), _on(v_pages, "v_pages", index, None, dtype), shape, code
 
 
 def medusa_pages_init(pages: Pages, stream=None):
     """Every page free, every row empty."""
-    _check(_lib.medusa_pages_init(pages.ref, _stream_on(stream, pages.device)), "medusa_pages_init")
+    _check(_lib.medusa_pages_init(pages.ref, _launch_on(stream, pages.index)), "medusa_pages_init")
 
 
 def medusa_pages_free(pages: Pages, keep_len, err=None, stream=None):
     """Rows with keep_len[r] >= 0 keep their first keep_len[r] tokens; keep_len [rows] int32."""
-    i32 = _i32()
-    _check(_lib.medusa_pages_free(pages.ref, _dense(keep_len, "keep_len", (pages.rows,), i32, pages),
-                                  _dense(err, "err", None, i32, pages), _stream_on(stream, pages.device)),
-           "medusa_pages_free")
+    d = pages.index
+    _check(_lib.medusa_pages_free(pages.ref, _ints(keep_len, "keep_len", d, pages.rows), _ints(err, "err", d),
+                                  _launch_on(stream, d)), "medusa_pages_free")
 
 
 def medusa_pages_fork(pages: Pages, src, dst, err=None, stream=None):
     """Row dst[i] (empty) becomes a second holder of row src[i]'s tokens; src, dst [n] int32."""
-    n, i32 = src.shape[0], _i32()
-    _check(_lib.medusa_pages_fork(pages.ref, _dense(src, "src", (n,), i32, pages),
-                                  _dense(dst, "dst", (n,), i32, pages), n, _dense(err, "err", None, i32, pages),
-                                  _stream_on(stream, pages.device)), "medusa_pages_fork")
+    d, n = pages.index, src.numel()
+    _check(_lib.medusa_pages_fork(pages.ref, _ints(src, "src", d), _ints(dst, "dst", d, n), n, _ints(err, "err", d),
+                                  _launch_on(stream, d)), "medusa_pages_fork")
 
 
 def medusa_pages_reserve(pages: Pages, n_new, copies, n_copies, granted=None, err=None, stream=None):
     """Room for n_new[r] more tokens per row; copies [>= rows][4] and n_copies [1] (int32) for medusa_pages_copy."""
-    i32 = _i32()
-    _check(_lib.medusa_pages_reserve(pages.ref, _dense(n_new, "n_new", (pages.rows,), i32, pages),
-                                     _dense(copies, "copies", (copies.shape[0], 4), i32, pages), copies.shape[0],
-                                     _dense(n_copies, "n_copies", (1,), i32, pages),
-                                     _dense(granted, "granted", (pages.rows,), i32, pages),
-                                     _dense(err, "err", None, i32, pages), _stream_on(stream, pages.device)),
-           "medusa_pages_reserve")
+    d = pages.index
+    _check(_lib.medusa_pages_reserve(pages.ref, _ints(n_new, "n_new", d, pages.rows), _ints(copies, "copies", d),
+                                     _lines(copies), _ints(n_copies, "n_copies", d, 1),
+                                     _ints(granted, "granted", d, pages.rows), _ints(err, "err", d),
+                                     _launch_on(stream, d)), "medusa_pages_reserve")
 
 
 def medusa_pages_commit(pages: Pages, rows, n_new, bias: int = 0, err=None, stream=None):
     """length[rows[b]] += n_new[b] + bias (rows None: row b)."""
-    B, i32 = n_new.shape[0], _i32()
-    _check(_lib.medusa_pages_commit(pages.ref, _dense(rows, "rows", (B,), i32, pages),
-                                    _dense(n_new, "n_new", (B,), i32, pages), int(bias), B,
-                                    _dense(err, "err", None, i32, pages), _stream_on(stream, pages.device)),
-           "medusa_pages_commit")
+    d, B = pages.index, n_new.numel()
+    _check(_lib.medusa_pages_commit(pages.ref, _ints(rows, "rows", d, B), _ints(n_new, "n_new", d), bias, B,
+                                    _ints(err, "err", d), _launch_on(stream, d)), "medusa_pages_commit")
 
 
 def medusa_pages_compact_workspace_size(num_pages: int) -> int:
@@ -610,24 +632,20 @@ def medusa_pages_compact_workspace_size(num_pages: int) -> int:
 
 def medusa_pages_compact(pages: Pages, copies, n_copies, workspace, err=None, stream=None):
     """The live pages to the front of the pool; copies [max_copies][4] and n_copies [1] for medusa_pages_copy."""
-    i32 = _i32()
-    _check(_lib.medusa_pages_compact(pages.ref, _dense(copies, "copies", (copies.shape[0], 4), i32, pages),
-                                     copies.shape[0], _dense(n_copies, "n_copies", (1,), i32, pages),
-                                     _dense(workspace, "workspace", None, None, pages),
-                                     workspace.numel() * workspace.element_size(),
-                                     _dense(err, "err", None, i32, pages), _stream_on(stream, pages.device)),
-           "medusa_pages_compact")
+    d = pages.index
+    _check(_lib.medusa_pages_compact(pages.ref, _ints(copies, "copies", d), _lines(copies),
+                                     _ints(n_copies, "n_copies", d, 1), _on(workspace, "workspace", d),
+                                     workspace.numel() * workspace.element_size(), _ints(err, "err", d),
+                                     _launch_on(stream, d)), "medusa_pages_compact")
 
 
 def medusa_pages_copy(k_pages, v_pages, copies, n_copies, err=None, stream=None):
     """Carry out a list of page copies in one layer's pools [num_pages][Hkv][page_size][Dh]."""
-    n, Hkv, ps, Dh, dt = _pool(k_pages, v_pages)
-    i32 = _i32()
-    _check(_lib.medusa_pages_copy(_dense(k_pages, "k_pages"), _dense(v_pages, "v_pages", None, None, k_pages), n, ps,
-                                  Hkv, Dh, dt, _dense(copies, "copies", (copies.shape[0], 4), i32, k_pages),
-                                  _dense(n_copies, "n_copies", (1,), i32, k_pages), copies.shape[0],
-                                  _dense(err, "err", None, i32, k_pages), _stream_on(stream, k_pages.device)),
-           "medusa_pages_copy")
+    d = k_pages.get_device()
+    kp, vp, (n, Hkv, ps, Dh), dt = _pool(k_pages, v_pages, d)
+    _check(_lib.medusa_pages_copy(kp, vp, n, ps, Hkv, Dh, dt, _ints(copies, "copies", d),
+                                  _ints(n_copies, "n_copies", d, 1), _lines(copies), _ints(err, "err", d),
+                                  _launch_on(stream, d)), "medusa_pages_copy")
 
 
 def medusa_paged_attn_workspace_size(B, total_q, max_new, H, Hkv, Dh, dtype) -> int:
@@ -638,15 +656,14 @@ def medusa_paged_attn_workspace_size(B, total_q, max_new, H, Hkv, Dh, dtype) -> 
                                                      MEDUSA_BF16 if dtype == torch.bfloat16 else MEDUSA_F32))
 
 
-def _heads(t, name, heads, Dh, total, dtype, pages):
+def _heads(t, name, shape, dtype, index):
     """Pointer and token stride of [total][heads][Dh], whose tokens may lie any distance apart."""
-    if t.shape != (total, heads, Dh):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(total, heads, Dh)}")
     st = t.stride()
-    if total and (st[2] != 1 or (heads > 1 and st[1] != Dh)):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}; expected {shape} {dtype} on the cache's "
+                         f"device")
+    if shape[0] and (st[2] != 1 or (st[1] != shape[2] and shape[1] > 1)):
         raise ValueError(f"{name}: a token's heads must lie side by side (strides {st})")
-    if t.dtype != dtype or t.device != pages.device:
-        raise TypeError(f"{name}: {t.dtype} on {t.device}, the pools are {dtype} on {pages.device}")
     return t.data_ptr(), st[0]
 
 
@@ -655,32 +672,29 @@ def medusa_paged_attn(q, k_new, v_new, k_pages, v_pages, pages: Pages, rows, q_s
     """A chunk of new tokens per sequence over the paged cache: q [total][H][Dh], k_new, v_new [total][Hkv][Dh]
     (tokens may be strided), q_start [B+1], rows [B] or None, tree a DeviceTree or None (causal), out
     [total][H][Dh]."""
-    _, Hkv, _, Dh, dt = _pool(k_pages, v_pages, pages)
-    total, H = q.shape[0], q.shape[1]
-    B = q_start.shape[0] - 1
-    ty, i32 = k_pages.dtype, _i32()
-    qp, qs = _heads(q, "q", H, Dh, total, ty, pages)
-    kp, ks = _heads(k_new, "k_new", Hkv, Dh, total, ty, pages)
-    vp, vs = _heads(v_new, "v_new", Hkv, Dh, total, ty, pages)
-    _check(_lib.medusa_paged_attn(qp, qs, kp, ks, vp, vs, _dense(k_pages, "k_pages", None, None, pages),
-                                  _dense(v_pages, "v_pages", None, None, pages), pages.ref,
-                                  _dense(rows, "rows", (B,), i32, pages), _dense(q_start, "q_start", None, i32, pages),
-                                  B, total, max_new, None if tree is None else tree.ref, H, Hkv, Dh, rope_theta, scale,
-                                  dt, _dense(out, "out", (total, H, Dh), ty, pages),
-                                  _dense(workspace, "workspace", None, None, pages),
-                                  workspace.numel() * workspace.element_size(), _dense(err, "err", None, i32, pages),
-                                  _stream_on(stream, pages.device)), "medusa_paged_attn")
+    d = pages.index
+    kc, vc, (_, Hkv, _, Dh), dt = _pool(k_pages, v_pages, d, pages)
+    total, H, _ = q.shape
+    B, ty = q_start.numel() - 1, k_pages.dtype
+    kv = (total, Hkv, Dh)
+    qp, qs = _heads(q, "q", (total, H, Dh), ty, d)
+    kp, ks = _heads(k_new, "k_new", kv, ty, d)
+    vp, vs = _heads(v_new, "v_new", kv, ty, d)
+    _check(_lib.medusa_paged_attn(qp, qs, kp, ks, vp, vs, kc, vc, pages.ref, _ints(rows, "rows", d, B),
+                                  _ints(q_start, "q_start", d), B, total, max_new,
+                                  None if tree is None else tree.ref, H, Hkv, Dh, rope_theta, scale, dt,
+                                  _on(out, "out", d, total * H * Dh, ty), _on(workspace, "workspace", d),
+                                  workspace.numel() * workspace.element_size(), _ints(err, "err", d),
+                                  _launch_on(stream, d)), "medusa_paged_attn")
 
 
 def medusa_paged_compact(k_pages, v_pages, pages: Pages, rows, accepted_nodes, accept_len, T: int, err=None,
                          stream=None):
     """The accepted path's keys and values into place inside the rows' pages, one layer; lengths stay."""
-    _, Hkv, _, Dh, dt = _pool(k_pages, v_pages, pages)
-    (B, Kp), i32 = accepted_nodes.shape, _i32()
-    _check(_lib.medusa_paged_compact(_dense(k_pages, "k_pages", None, None, pages),
-                                     _dense(v_pages, "v_pages", None, None, pages), pages.ref,
-                                     _dense(rows, "rows", (B,), i32, pages),
-                                     _dense(accepted_nodes, "accepted_nodes", None, i32, pages),
-                                     _dense(accept_len, "accept_len", (B,), i32, pages), B, Hkv, Dh, Kp - 1, T, dt,
-                                     _dense(err, "err", None, i32, pages), _stream_on(stream, pages.device)),
+    d = pages.index
+    kc, vc, (_, Hkv, _, Dh), dt = _pool(k_pages, v_pages, d, pages)
+    B, Kp = accepted_nodes.shape
+    _check(_lib.medusa_paged_compact(kc, vc, pages.ref, _ints(rows, "rows", d, B),
+                                     _ints(accepted_nodes, "accepted_nodes", d), _ints(accept_len, "accept_len", d, B),
+                                     B, Hkv, Dh, Kp - 1, T, dt, _ints(err, "err", d), _launch_on(stream, d)),
            "medusa_paged_compact")

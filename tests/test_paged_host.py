@@ -122,7 +122,7 @@ def test_binding_refuses_tensors_that_do_not_fit(M):
             M.Pages.from_state(bad, 4, 2, 8, 16)
     with pytest.raises(ValueError, match="keep_len"):
         M.medusa_pages_free(p, torch.zeros(3, dtype=torch.int32))
-    with pytest.raises(TypeError, match="keep_len"):
+    with pytest.raises(ValueError, match="keep_len"):
         M.medusa_pages_free(p, torch.zeros(4, dtype=torch.int64))
     with pytest.raises(ValueError, match="current CUDA device"):
         M.medusa_pages_free(p, torch.zeros(4, dtype=torch.int32))
@@ -135,7 +135,7 @@ def test_binding_refuses_tensors_that_do_not_fit(M):
                 workspace=torch.zeros(1, dtype=torch.uint8))
     with pytest.raises(ValueError, match="k_new"):
         M.medusa_paged_attn(qkv[:, :4], qkv[:, 4:7], qkv[:, 6:], **args)
-    with pytest.raises(TypeError, match="q: "):
+    with pytest.raises(ValueError, match="q: "):
         M.medusa_paged_attn(qkv[:, :4].float(), qkv[:, 4:6], qkv[:, 6:], **args)
     with pytest.raises(ValueError, match="side by side"):
         M.medusa_paged_attn(qkv[:, ::2], qkv[:, 4:6], qkv[:, 6:], **args)
