@@ -150,11 +150,10 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   int64_t x, x1;
   make_plan<kGenThreads, RB, KT>(a, sc, pl, x, x1);
-  if (x >= x1) return;
   const int64_t total = pl.total, grid = min((int64_t)gridDim.x, total);
   const int tb = RB / a.g;
   Segment sg;
-  seek_segment<RB, KT>(a, sc, x, x1, sg);
+  if (x >= x1 || !seek_segment<RB, KT>(a, sc, x, x1, sg)) return;
   while (true) {
     const SeqInfo& s = sg.s;
     const int nkeys = s.L + s.n, tok0 = sg.u * tb, live = min(tb, s.n - tok0) * a.g;
@@ -339,9 +338,7 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
         }
       }
     }
-    x += sg.t1 - sg.t0;
-    if (x >= x1) break;
-    next_segment<RB, KT>(a, pl, x, x1, sg);
+    if (!next_segment<RB, KT>(a, pl, x1, sg)) break;
   }
 }
 

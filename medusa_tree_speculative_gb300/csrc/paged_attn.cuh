@@ -5,10 +5,14 @@
 // sequence's key head is token r / g, head r % g, and a block holds whole
 // tokens (RB / g of them), so that one pass over the keys serves all g heads.
 // A unit reads the key tiles its last token sees.  All units' tiles, in the
-// order (sequence, key head, block, tile), form one list, which the grid's
-// CTAs share out evenly: CTA c of G takes tiles [c N / G, (c + 1) N / G).  So
-// ragged batches, one long sequence and a causal triangle are balanced alike,
-// and nothing about the lengths is needed on the host.  A unit that several
+// order (sequence, key head, block, tile), form one list, in which each unit
+// also has kUnitCost empty places before its first tile, for the time that
+// beginning and ending a unit takes.  The grid's CTAs share the list's N
+// places out evenly: CTA c of G takes [c N / G, (c + 1) N / G).  So ragged
+// batches, one long sequence and a causal triangle are balanced alike, and
+// nothing about the lengths is needed on the host.  (Without the empty places
+// the CTAs with a causal triangle's short units ran a third longer than the
+// mean.)  A unit that several
 // CTAs share is joined by the last of them to finish (an arrival counter);
 // every partial goes through the workspace and is added in CTA order, whoever
 // adds it, so the result does not depend on timing.
@@ -28,6 +32,7 @@ namespace medusa {
 constexpr int kPagedMaxGroup = 64;     // query heads per key head
 constexpr int kFewRows = 16;           // rows (tokens x heads of a key head) of the kernels for few rows
 constexpr int kPagedCounters = 1024;   // arrival counters of one kernel
+constexpr int kUnitCost = 2;           // places in the list of work that a unit has besides its tiles
 constexpr float kPagedLog2e = 1.4426950408889634f;
 
 struct PagedAttnArgs {
@@ -88,15 +93,15 @@ MDEV int unit_tiles(const PagedAttnArgs& a, const SeqInfo& s, int tb, int u) {
   const int seen = a.T ? s.n : min(s.n, (u + 1) * tb);
   return (s.L + seen + KT - 1) / KT;
 }
-// Sum of unit_tiles over blocks 0 .. u-1, all of them full: sum over i of
+// Places of blocks 0 .. u-1, all of them full: u kUnitCost and the sum over i of
 // floor((L + (i + 1) tb + KT - 1) / KT), by Euclid's reduction of the sum of
 // floor((A i + C) / M) (lattice points below a line).
 template <int KT>
-MDEV int64_t tiles_before(const PagedAttnArgs& a, const SeqInfo& s, int tb, int u) {
+MDEV int64_t places_before(const PagedAttnArgs& a, const SeqInfo& s, int tb, int u) {
   if (u <= 0) return 0;
-  if (a.T) return (int64_t)u * ((s.L + s.n + KT - 1) / KT);
+  if (a.T) return (int64_t)u * ((s.L + s.n + KT - 1) / KT + kUnitCost);
   uint64_t n = (uint64_t)u, m = KT, x = (uint64_t)tb, c = (uint64_t)s.L + tb + KT - 1;
-  int64_t sum = 0;
+  int64_t sum = (int64_t)u * kUnitCost;
   while (true) {
     sum += (int64_t)((n - 1) * n / 2 * (x / m));
     x %= m;
@@ -112,34 +117,34 @@ MDEV int64_t tiles_before(const PagedAttnArgs& a, const SeqInfo& s, int tb, int 
   }
   return sum;
 }
-// Tiles of one key head of a sequence.
+// Places of one key head of a sequence.
 template <int KT>
-MDEV int64_t seq_tiles(const PagedAttnArgs& a, const SeqInfo& s, int tb) {
+MDEV int64_t seq_places(const PagedAttnArgs& a, const SeqInfo& s, int tb) {
   const int m = (s.n + tb - 1) / tb;
-  return tiles_before<KT>(a, s, tb, m - 1) + unit_tiles<KT>(a, s, tb, m - 1);
+  return places_before<KT>(a, s, tb, m - 1) + kUnitCost + unit_tiles<KT>(a, s, tb, m - 1);
 }
 
 // Shared memory for the plan: scratch, used only while it is made, and what
 // stays.
 struct PlanScratch {
   int owner[MEDUSA_MAX_ROWS];        // cache row -> the first entry that names it
-  int64_t pre[MEDUSA_MAX_ROWS + 1];  // tiles before each sequence
+  int64_t pre[MEDUSA_MAX_ROWS + 1];  // places before each sequence
+  int64_t warp_sum[32];
 };
 struct Plan {
   uint32_t valid[MEDUSA_MAX_ROWS / 32];  // the sequences that are not skipped
-  int64_t total;                         // tiles in all
-  int64_t warp_sum[33];
+  int64_t total;                         // places in all
 };
 
 // Where in the list a CTA stands: a unit and the tiles of it that are its own.
 struct Segment {
   SeqInfo s;
   int b, head, u, m, tiles;  // m blocks; tiles of this unit
-  int t0, t1;
-  int64_t unit_x;            // the unit's first tile in the list
+  int t0, t1;                // t0 < t1: there are no segments without tiles
+  int64_t unit_x;            // the unit's first place in the list
 };
 
-// Build the plan (all NT threads of the CTA); x0, x1: this CTA's tiles.
+// Build the plan (all NT threads of the CTA); x0, x1: this CTA's places.
 template <int NT, int RB, int KT>
 MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& x0, int64_t& x1) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -172,7 +177,7 @@ MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& 
     sc.pre[b] = mine;
     if (ok) {
       atomicOr(&pl.valid[b >> 5], 1u << (b & 31));
-      mine += (int64_t)a.Hkv * seq_tiles<KT>(a, s, tb);
+      mine += (int64_t)a.Hkv * seq_places<KT>(a, s, tb);
     }
   }
   int64_t x = mine;
@@ -181,11 +186,11 @@ MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& 
     const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) pl.warp_sum[warp] = x;
+  if (lane == 31) sc.warp_sum[warp] = x;
   __syncthreads();
   int64_t before = 0, total = 0;
   for (int w = 0; w < NT / 32; ++w) {
-    const int64_t v = pl.warp_sum[w];
+    const int64_t v = sc.warp_sum[w];
     if (w < warp) before += v;
     total += v;
   }
@@ -208,11 +213,20 @@ MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& 
   }
 }
 
-// The segment of the list that starts at tile x (x < x1).
+// The tiles of unit g in places [x, x1) of the list; false if there are none.
+MDEV bool set_tiles(Segment& g, int64_t x, int64_t x1) {
+  const int64_t tile0 = g.unit_x + kUnitCost;
+  g.t0 = (int)max((int64_t)0, x - tile0);
+  g.t1 = (int)min((int64_t)g.tiles, x1 - tile0);
+  return g.t0 < g.t1;
+}
+
+// The segment that place x of the list is in (x < x1); false if [x, x1) has no
+// tiles.
 template <int RB, int KT>
-MDEV void seek_segment(const PagedAttnArgs& a, const PlanScratch& sc, int64_t x, int64_t x1, Segment& g) {
+MDEV bool seek_segment(const PagedAttnArgs& a, const PlanScratch& sc, int64_t x, int64_t x1, Segment& g) {
   const int tb = RB / a.g;
-  int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before x: it has tiles, or total would be x
+  int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before x: it has places, or total would be x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (sc.pre[mid] <= x) lo = mid; else hi = mid - 1;
@@ -221,57 +235,54 @@ MDEV void seek_segment(const PagedAttnArgs& a, const PlanScratch& sc, int64_t x,
   int code;
   seq_info(a, lo, g.s, code);
   g.m = (g.s.n + tb - 1) / tb;
-  const int64_t each = seq_tiles<KT>(a, g.s, tb);
+  const int64_t each = seq_places<KT>(a, g.s, tb);
   int64_t rest = x - sc.pre[lo];
   g.head = (int)(rest / each);
   rest -= (int64_t)g.head * each;
   int ulo = 0, uhi = g.m - 1;
   while (ulo < uhi) {
     const int mid = (ulo + uhi + 1) >> 1;
-    if (tiles_before<KT>(a, g.s, tb, mid) <= rest) ulo = mid; else uhi = mid - 1;
+    if (places_before<KT>(a, g.s, tb, mid) <= rest) ulo = mid; else uhi = mid - 1;
   }
   g.u = ulo;
-  rest -= tiles_before<KT>(a, g.s, tb, ulo);
+  rest -= places_before<KT>(a, g.s, tb, ulo);
   g.tiles = unit_tiles<KT>(a, g.s, tb, ulo);
   g.unit_x = x - rest;
-  g.t0 = (int)rest;
-  g.t1 = (int)min((int64_t)g.tiles, rest + (x1 - x));
+  return set_tiles(g, x, x1);
 }
 
-// The segment after g (which ended at its unit's end), starting at tile x.
+// The segment after g; false if this CTA's places before x1 have none.
 template <int RB, int KT>
-MDEV void next_segment(const PagedAttnArgs& a, const Plan& pl, int64_t x, int64_t x1, Segment& g) {
+MDEV bool next_segment(const PagedAttnArgs& a, const Plan& pl, int64_t x1, Segment& g) {
   const int tb = RB / a.g;
+  g.unit_x += g.tiles + kUnitCost;
+  if (g.unit_x >= x1) return false;
   if (++g.u == g.m) {
     g.u = 0;
     if (++g.head == a.Hkv) {
       g.head = 0;
       do ++g.b; while (g.b < a.B && !(pl.valid[g.b >> 5] >> (g.b & 31) & 1u));
-      if (g.b >= a.B) {  // not reached: x < x1 <= total
-        g.t0 = g.t1 = 0;
-        return;
-      }
+      if (g.b >= a.B) return false;  // not reached: unit_x < x1 <= total
       int code;
       seq_info(a, g.b, g.s, code);
       g.m = (g.s.n + tb - 1) / tb;
     }
   }
   g.tiles = unit_tiles<KT>(a, g.s, tb, g.u);
-  g.unit_x = x;
-  g.t0 = 0;
-  g.t1 = (int)min((int64_t)g.tiles, x1 - x);
+  return set_tiles(g, g.unit_x, x1);
 }
 
-// CTA that holds tile x of the list.
+// CTA that holds place x of the list.
 MDEV int cta_of(int64_t x, int64_t total, int64_t G) { return (int)(((x + 1) * G - 1) / total); }
 
 // Who shares the unit of g: its first and last CTA.
 MDEV void unit_shares(const Segment& g, int64_t total, int64_t G, int& first, int& last) {
-  first = cta_of(g.unit_x, total, G);
-  last = cta_of(g.unit_x + g.tiles - 1, total, G);
+  first = cta_of(g.unit_x + kUnitCost, total, G);
+  last = cta_of(g.unit_x + kUnitCost + g.tiles - 1, total, G);
 }
 // Slot (of two) of CTA c's partial of the unit that starts at unit_x: 0 if it
-// is the CTA's first segment, else 1.
+// is the CTA's first segment, else 1 (a CTA that starts in an earlier unit has
+// that one's last tile).
 MDEV int part_slot(int64_t unit_x, int c, int64_t total, int64_t G) {
   const int64_t x0 = (int64_t)c * total / G;
   return 2 * c + (x0 >= unit_x ? 0 : 1);

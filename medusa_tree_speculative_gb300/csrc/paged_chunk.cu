@@ -9,9 +9,12 @@
 // thread's order is PV0(j), QK0(j+1), PV1(j), QK1(j+1), ..., so a lane's
 // softmax has the other lane's two products, 1024 cycles, to hide behind.  The
 // kernel is bound by the tensor core where that holds.
-//   * warps 0-3 and 4-7 are the lanes' softmax: a thread per query row (its
-//     tensor-memory lane) reads 128 scores, and writes P = 2^(S - m) in bf16
-//     over them in tensor memory; no exchange between threads.
+//   * warps 0-7 and 8-15 are the lanes' softmax, two threads per query row
+//     (its tensor-memory lane), one per half of the tile's keys: each reads 64
+//     scores, the two agree on the row's maximum through shared memory, and
+//     write P = 2^(S - m) in bf16 over the scores in tensor memory.  One thread
+//     per row took 1700 cycles from scores to P, 660 more than the other
+//     lane's products hide.
 //   * O stays in tensor memory.  The base m of a row only moves when the
 //     row's maximum passes it by more than 8 (P is at most 2^8, its sum is
 //     kept in 32 bits), so O is rescaled a few times per row and not per tile.
@@ -36,46 +39,65 @@ namespace {
 using namespace sm100;
 
 constexpr int RB = 256, KT = 128;
-constexpr int kThreads = 384;  // two softmax groups; the load warp, the MMA warp and two idle ones
-// Registers: the block starts with 168 a thread (384 x 168 = 64512); the
-// softmax threads, which hold 128 scores each, then take what the third group
-// gives up: 256 x 208 + 128 x 88 = 64512.
-constexpr int kLaunchRegs = 168, kSoftRegs = 208, kOtherRegs = 88;
-static_assert(256 * kSoftRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "registers");
+constexpr int kThreads = 640;  // two softmax groups of 256; the load warp, the MMA warp and two segment warps
+constexpr int kSoft = 512, kLoadWarp = 16, kMmaWarp = 17;
+// Registers: the block starts with 96 a thread (640 x 96 = 61440); the softmax
+// threads then take what the other warps give up: 512 x 104 + 128 x 64.
+constexpr int kLaunchRegs = 96, kSoftRegs = 104, kOtherRegs = 64;
+static_assert(kSoft * kSoftRegs + (kThreads - kSoft) * kOtherRegs <= kThreads * kLaunchRegs, "registers");
 constexpr uint32_t kTmemCols = 512;
+
+template <uint32_t B>
+struct Half {
+  static constexpr uint32_t value = B;
+};
 
 template <int DH>
 struct Cfg {
   static constexpr int kHalves = DH / 64;
   static constexpr uint32_t kHalf = 128 * 128;          // 128 rows of one swizzle span
   static constexpr uint32_t kTile = kHalf * kHalves;    // 128 rows x DH bf16
-  static constexpr int kSlots = DH == 128 ? 5 : 10;
+  static constexpr int kSlots = 4;  // K, V of an even tile, K, V of an odd one: their addresses are constants
   static constexpr uint32_t kRingOff = 2 * kTile;
   static constexpr uint32_t kBarOff = kRingOff + kSlots * kTile;
-  static constexpr int kBars = 2 * kSlots + 2 + 2 + 2 + 1 + 1;
-  static constexpr uint32_t kPlanOff = (kBarOff + kBars * 8 + 16 + 15) & ~15u;
-  static constexpr uint32_t kMlOff = (kPlanOff + sizeof(Plan) + 15) & ~15u;  // [2 lanes][128 rows] (max, sum)
-  static constexpr size_t smem = kMlOff + 2 * 128 * 8;
+  static constexpr int kBars = 2 * kSlots + 2 + 2 + 2 + 1 + 1 + 1;
+  static constexpr uint32_t kSegOff = (kBarOff + kBars * 8 + 16 + 15) & ~15u;    // [2 lanes][2] segments
+  static constexpr uint32_t kPlanOff = (kSegOff + 4 * sizeof(Segment) + 15) & ~15u;
+  static constexpr uint32_t kRowOff = (kPlanOff + sizeof(Plan) + 15) & ~15u;  // [2 lanes][128 rows] 8 bytes
+  static constexpr size_t smem = kRowOff + 2 * 128 * 8;
   static_assert(smem <= 232448, "shared memory");
   static constexpr int part_floats = 128 * DH + 2 * 128;  // one lane's partial
   static_assert(sizeof(PlanScratch) <= kSlots * kTile, "the plan's scratch lies in the ring");
 };
 
-MDEV uint64_t desc_mnmajor(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// One thread of a converged warp, the same one every time.  The MMA's operands
+// are warp-wide registers: behind an `elect` the compiler knows that one thread
+// issues, behind a comparison of the lane it goes through the lanes one by one.
+MDEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
 }
 MDEV void fence_smem_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
-MDEV void bar_group(int lane_id) {
-  if (lane_id == 0) asm volatile("bar.sync 1, 128;\n" ::: "memory");
-  else asm volatile("bar.sync 2, 128;\n" ::: "memory");
+// Barriers of a row quarter's two warps, of a lane's 256 threads, of all 512.
+MDEV void bar_pair(int i, int q) { asm volatile("bar.sync %0, 64;\n" ::"r"(1 + i * 4 + q) : "memory"); }
+MDEV bool bar_pair_any(int i, int q, bool flag) {
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred f, r;\n\tsetp.ne.s32 f, %1, 0;\n\tbarrier.red.or.pred r, %2, 64, f;\n\tselp.s32 %0, 1, 0, r;\n\t}\n"
+      : "=r"(any)
+      : "r"((int)flag), "r"(1 + i * 4 + q)
+      : "memory");
+  return any != 0;
 }
-MDEV void bar_both() { asm volatile("bar.sync 3, 256;\n" ::: "memory"); }
+MDEV void bar_lane(int i) { asm volatile("bar.sync %0, 256;\n" ::"r"(9 + i) : "memory"); }
+// A lane's threads and the warp that writes its segments.
+MDEV void bar_segment(int i) { asm volatile("bar.sync %0, 288;\n" ::"r"(12 + i) : "memory"); }
+MDEV void bar_all() { asm volatile("bar.sync 11, 512;\n" ::: "memory"); }
 MDEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -99,16 +121,46 @@ MDEV void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-MDEV void tmem_st32(uint32_t taddr, const uint32_t* r) {
+// MMAs from descriptor words (both descriptors' high words are the same), tensor
+// memory from column 0: a block that allocates all 512 columns gets them there.
+MDEV void umma_words(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "{\n\t.reg .pred p;\n\t.reg .b64 A, B;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 A, {%1, %3};\n\tmov.b64 B, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], A, B, %4, p;\n\t}\n" ::"r"(d),
+      "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(add)
       : "memory");
+}
+MDEV void umma_ts_words(uint32_t d, uint32_t a, uint32_t blo, uint32_t hi, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 B;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 B, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], B, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(blo), "r"(hi), "r"(idesc), "r"(add)
+      : "memory");
+}
+MDEV void commit_at(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+MDEV bool try_wait_at(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// paged_wait by shared-memory address.
+MDEV void wait_at(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (try_wait_at(bar, parity)) return;
+  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    if (try_wait_at(bar, parity)) return;
+    if ((i & 63) == 63 && *abort_flag) return;
+  }
+  *abort_flag = 1;
 }
 
 template <int DH>
@@ -126,15 +178,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* empty = full + G::kSlots;                               // [slots] MMA -> TMA
   uint64_t* s_full = empty + G::kSlots;                             // [2] MMA -> softmax: scores
   uint64_t* p_full = s_full + 2;                                    // [2] softmax -> MMA: P written, O rescaled
-  uint64_t* pv_done = p_full + 2;                                   // [2] MMA -> softmax: O up to date
+  uint64_t* pv_done = p_full + 2;                                   // [2] MMA -> softmax: the segment's O is complete
   uint64_t* q_full = pv_done + 2;
-  uint64_t* all_done = q_full + 1;
+  uint64_t* q_empty = q_full + 1;                                   // MMA -> TMA: every product of these queries is done
+  uint64_t* all_done = q_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + 1);
   int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
   int* s_flag = s_abort + 1;  // [2]
   Plan& pl = *reinterpret_cast<Plan*>(smem + G::kPlanOff);
   PlanScratch& sc = *reinterpret_cast<PlanScratch*>(smem + G::kRingOff);
-  float2* xml = reinterpret_cast<float2*>(smem + G::kMlOff);
+  Segment* segs = reinterpret_cast<Segment*>(smem + G::kSegOff);
   volatile int* abort_flag = s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -144,10 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 8);
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     mbar_init(all_done, 1);
     fence_barrier_init();
     *s_abort = 0;
@@ -155,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -163,16 +217,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   make_plan<kThreads, RB, KT>(a, sc, pl, x0, x1);
   const int64_t total = pl.total, grid = min((int64_t)gridDim.x, total);
   Segment sg;
-  if (x0 < x1) seek_segment<RB, KT>(a, sc, x0, x1, sg);
+  const bool any = x0 < x1 && seek_segment<RB, KT>(a, sc, x0, x1, sg);
   fence_smem_async();  // the scratch was read and written; the ring's copies follow
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *tmem_slot;  // 0: all of it
   const int tb = RB / a.g;
-  if (warp >= 8) {
+  if (warp >= kSoft / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-    if (warp == 8 && x0 < x1) {
+    if (warp == kLoadWarp && any) {
       // ------------------------------------------------ keys and values
       asm volatile("fence.proxy.async.global;\n" ::: "memory");  // the appended tokens, written by the launch before
       const int box = min(a.p.page_size, KT), runs = KT / box;
@@ -180,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = op_run < runs;
       const int nowhere = (a.p.num_pages * a.Hkv) << a.p.shift;  // past the pool: reads zeros
       int n = 0;
-      for (int64_t x = x0;;) {
+      while (true) {
         const SeqInfo& s = sg.s;
         const int nkeys = s.L + s.n;
         for (int t = sg.t0; t < sg.t1; ++t) {
@@ -202,316 +256,416 @@ __global__ void __launch_bounds__(kThreads, 1)
                           kv ? &tmV : &tmK, &full[sl], op_half * 64, y);
           }
         }
-        x += sg.t1 - sg.t0;
-        if (x >= x1) break;
-        next_segment<RB, KT>(a, pl, x, x1, sg);
+        if (!next_segment<RB, KT>(a, pl, x1, sg)) break;
       }
       // the copies in flight land before the CTA can end, whatever happened
       for (int j = max(0, n - G::kSlots); j < n; ++j)
         if (!mbar_wait(&full[j % G::kSlots], (uint32_t)(j / G::kSlots) & 1u)) *abort_flag = 1;
-    } else if (warp == 9 && x0 < x1) {
-      // ------------------------------------------------ MMAs and query tiles
-      if (lane == 0) {
-        const uint32_t idS = idesc_bf16_f32(128, KT);
-        const uint32_t idPV = idesc_bf16_f32(128, DH) | (1u << 16);  // V as stored, keys x values: MN-major
-        int nq = 0, it = 0;
-        uint32_t cnt[2] = {0, 0};  // this lane's tiles so far
-        auto live_of = [&](const Segment& g) { return min(tb, g.s.n - g.u * tb) * a.g; };
-        auto load_q = [&](const Segment& g) {
-          const int tiles = live_of(g) > 128 ? 2 : 1;
-          const int y = (g.head * a.total_q + g.s.q0 + g.u * tb) * a.g;
-          mbar_expect_tx(q_full, tiles * G::kTile);
-          for (int i = 0; i < tiles; ++i)
-            for (int h = 0; h < G::kHalves; ++h)
-              tma_load_2d(smem + i * G::kTile + h * G::kHalf, &tmQ, q_full, h * 64, y + i * 128);
-        };
-        auto wait_kv = [&](int n) { paged_wait(&full[n % G::kSlots], (uint32_t)(n / G::kSlots) & 1u, abort_flag); };
-        auto free_kv = [&](int n) { umma_commit(&empty[n % G::kSlots]); };
-        auto qk = [&](int i, int qt, int t) {  // lane i's scores of tile t (of the CTA's count) from query tile qt
-          const uint32_t k = sbase + G::kRingOff + (uint32_t)((2 * t) % G::kSlots) * G::kTile;
+    } else if (warp == kMmaWarp && any) {
+      // ------------------------------------------------ MMAs
+      // One warp issues 32 products' instructions per tile of 2048 cycles and
+      // competes with the softmax warps for issue slots, so this loop is kept
+      // short: addresses are constants (two tiles' ring slots in turn), what the
+      // MMAs read is the same in every lane for the compiler to see
+      // (warp-wide registers), barriers are waited for ahead of need, and there
+      // are as few commits as will do: QK(j+1)'s also says that PV(j), issued
+      // before it, is done.
+      auto uni = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+      constexpr uint32_t idS = idesc_bf16_f32(128, KT);
+      constexpr uint32_t idPV = idesc_bf16_f32(128, DH) | (1u << 16);  // V as stored, keys x values: MN-major
+      // matrix descriptors: 128-byte swizzle, 1024 bytes between 8-row groups;
+      // low word: address / 16 and, for V, the bytes / 16 between its halves
+      constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+      constexpr uint32_t kTile16 = G::kTile >> 4, kHalf16 = G::kHalf >> 4;
+      const uint32_t q16 = (sbase >> 4) | 1u << 16, k16 = ((sbase + G::kRingOff) >> 4) | 1u << 16;
+      const uint32_t v16 = ((sbase + G::kRingOff) >> 4) + kTile16 | kHalf16 << 16;
+      const uint32_t bars = smem_u32(full);
+      constexpr uint32_t kEmpty = 4 * 8, kS = 8 * 8, kP = 10 * 8, kPV = 12 * 8, kQ = 14 * 8, kQE = 15 * 8;
+      auto qk = [&](uint32_t d, uint32_t qa, uint32_t ka) {
 #pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk) {
-            const uint64_t da = desc_kmajor_sw128(sbase + qt * G::kTile + (kk >> 2) * G::kHalf) + (uint64_t)((kk & 3) * 2);
-            const uint64_t db = desc_kmajor_sw128(k + (kk >> 2) * G::kHalf) + (uint64_t)((kk & 3) * 2);
-            umma_bf16(tmem + i * 128, da, db, idS, kk != 0);
-          }
-          umma_commit(&s_full[i]);
-        };
-        auto pv = [&](int i, int t, bool add) {
-          const uint32_t v = sbase + G::kRingOff + (uint32_t)((2 * t + 1) % G::kSlots) * G::kTile;
+        for (int kk = 0; kk < DH / 16; ++kk)
+          umma_words(d, qa + (kk >> 2) * kHalf16 + (kk & 3) * 2, ka + (kk >> 2) * kHalf16 + (kk & 3) * 2, kDescHi, idS,
+                     kk != 0);
+      };
+      auto pv = [&](uint32_t d, uint32_t va, uint32_t add) {
 #pragma unroll
-          for (int j = 0; j < KT / 16; ++j)
-            umma_bf16_ts(tmem + 256 + i * 128, tmem + i * 128 + j * 8, desc_mnmajor(v + j * 2048, G::kHalf, 1024), idPV,
-                         add || j != 0);
-          umma_commit(&pv_done[i]);
-        };
-        auto wait_p = [&](int i) {
-          paged_wait(&p_full[i], cnt[i] & 1u, abort_flag);
-          ++cnt[i];
-          tc_fence_after();
-        };
-        load_q(sg);
-        for (int64_t x = x0;; ++nq) {
-          const int nt = sg.t1 - sg.t0;
-          const bool wide = live_of(sg) > 128;
-          paged_wait(q_full, (uint32_t)nq & 1u, abort_flag);
-          if (wide) {
-            wait_kv(2 * it);
+        for (int j = 0; j < KT / 16; ++j)
+          umma_ts_words(256 + d, d + j * 8, va + j * (2048 >> 4), kDescHi, idPV, j == 0 ? add : 1u);
+      };
+      uint32_t t = 0, ph0 = 0, ph1 = 0, qph = 0;  // the CTA's tiles so far; phases of p_full and q_full
+      uint32_t nt = 0, wide = 0;
+      auto enter = [&]() {
+        nt = uni(sg.t1 - sg.t0);
+        wide = uni(min(tb, sg.s.n - sg.u * tb) * a.g > 128);
+      };
+      enter();
+      bool ready = false;  // the segment's first scores are on their way
+      while (true) {
+        const uint32_t n = nt, w = wide;
+        const uint32_t more = uni(next_segment<RB, KT>(a, pl, x1, sg));
+        if (more) enter();
+        const bool chain = more && w && wide;  // the next segment's first scores follow this one's last
+        if (!ready) {
+          wait_at(bars + kQ, qph, abort_flag);
+          qph ^= 1u;
+          for (uint32_t i = 0; i < 2 && (w ? i < 1 : i < n); ++i) {
+            const uint32_t b = uni((t + i) & 1u);
+            wait_at(bars + b * 16, (t + i) >> 1 & 1u, abort_flag);
             tc_fence_after();
-            qk(0, 0, it);
-            qk(1, 1, it);
-            free_kv(2 * it);
-            for (int j = 0; j < nt; ++j) {
-              const bool more = j + 1 < nt;
-              wait_p(0);
-              wait_kv(2 * (it + j) + 1);
-              pv(0, it + j, j > 0);
-              if (more) {
-                wait_kv(2 * (it + j + 1));
-                tc_fence_after();
-                qk(0, 0, it + j + 1);
+            if (elect_one()) {
+              qk(i * 128, q16, k16 + b * 2 * kTile16);
+              commit_at(bars + kS + i * 8);
+              if (w) {
+                qk(128, q16 + kTile16, k16 + b * 2 * kTile16);
+                commit_at(bars + kS + 8);
               }
-              wait_p(1);
-              pv(1, it + j, j > 0);
-              free_kv(2 * (it + j) + 1);
-              if (more) {
-                qk(1, 1, it + j + 1);
-                free_kv(2 * (it + j + 1));
-              }
+              commit_at(bars + kEmpty + b * 16);
+              if (w ? n == 1 : i + 1 == n) commit_at(bars + kQE);
             }
-          } else {
-            for (int i = 0; i < 2 && i < nt; ++i) {
-              wait_kv(2 * (it + i));
-              tc_fence_after();
-              qk(i, 0, it + i);
-              free_kv(2 * (it + i));
-            }
-            for (int j = 0; j < nt; ++j) {
-              const int i = j & 1;
-              wait_p(i);
-              wait_kv(2 * (it + j) + 1);
-              pv(i, it + j, j > 1);
-              free_kv(2 * (it + j) + 1);
-              if (j + 2 < nt) {
-                wait_kv(2 * (it + j + 2));
-                tc_fence_after();
-                qk(i, 0, it + j + 2);
-                free_kv(2 * (it + j + 2));
-              }
-            }
+            __syncwarp();
           }
-          it += nt;
-          x += nt;
-          if (x >= x1) break;
-          next_segment<RB, KT>(a, pl, x, x1, sg);
-          load_q(sg);  // the last waits for P say that every product of the old queries is done
         }
-        umma_commit(all_done);
-        if (!mbar_wait(all_done, 0)) *abort_flag = 1;
+        if (w) {
+          // tile t in ring half b: PV0, QK0 of the next, PV1, QK1 of the next
+          auto tile = [&](auto half, uint32_t j) {
+            constexpr uint32_t b = decltype(half)::value;
+            const bool end = j + 1 == n, go = !end || chain, qe = j + 2 == n || (end && chain && nt == 1);
+            wait_at(bars + b * 16 + 8, t >> 1 & 1u, abort_flag);  // ahead of P
+            wait_at(bars + kP, ph0, abort_flag);
+            tc_fence_after();
+            if (elect_one()) {
+              pv(0, v16 + b * 2 * kTile16, j > 0);
+              if (end) commit_at(bars + kPV);
+            }
+            __syncwarp();
+            if (go) {
+              if (end) {
+                wait_at(bars + kQ, qph, abort_flag);
+                qph ^= 1u;
+              }
+              wait_at(bars + (b ^ 1) * 16, (t + 1) >> 1 & 1u, abort_flag);
+              tc_fence_after();
+              if (elect_one()) {
+                qk(0, q16, k16 + (b ^ 1) * 2 * kTile16);
+                commit_at(bars + kS);
+              }
+              __syncwarp();
+            }
+            wait_at(bars + kP + 8, ph1, abort_flag);
+            tc_fence_after();
+            if (elect_one()) {
+              pv(128, v16 + b * 2 * kTile16, j > 0);
+              commit_at(bars + kEmpty + b * 16 + 8);
+              if (end) commit_at(bars + kPV + 8);
+              if (go) {
+                qk(128, q16 + kTile16, k16 + (b ^ 1) * 2 * kTile16);
+                commit_at(bars + kS + 8);
+                commit_at(bars + kEmpty + (b ^ 1) * 16);
+                if (qe) commit_at(bars + kQE);
+              }
+            }
+            __syncwarp();
+            ph0 ^= 1u;
+            ph1 ^= 1u;
+            ++t;
+          };
+          for (uint32_t j = 0; j < n; ++j) {
+            if (t & 1u) tile(Half<1>(), j);
+            else tile(Half<0>(), j);
+          }
+          ready = chain;
+        } else {
+          for (uint32_t j = 0; j < n; ++j) {
+            const uint32_t i = uni(j & 1u), b = uni(t & 1u);
+            wait_at(bars + b * 16 + 8, t >> 1 & 1u, abort_flag);
+            wait_at(bars + kP + i * 8, i ? ph1 : ph0, abort_flag);
+            if (i) ph1 ^= 1u; else ph0 ^= 1u;
+            tc_fence_after();
+            const bool go = j + 2 < n;
+            if (elect_one()) {
+              pv(i * 128, v16 + b * 2 * kTile16, j > 1);
+              commit_at(bars + kEmpty + b * 16 + 8);
+              if (!go) commit_at(bars + kPV + i * 8);
+            }
+            __syncwarp();
+            if (go) {
+              wait_at(bars + b * 16, (t + 2) >> 1 & 1u, abort_flag);
+              tc_fence_after();
+              if (elect_one()) {
+                qk(i * 128, q16, k16 + b * 2 * kTile16);
+                commit_at(bars + kS + i * 8);
+                commit_at(bars + kEmpty + b * 16);
+                if (j + 3 == n) commit_at(bars + kQE);
+              }
+              __syncwarp();
+            }
+            ++t;
+          }
+          ready = false;
+        }
+        if (!more) break;
       }
+      if (elect_one()) umma_commit(all_done);
+      if (!mbar_wait(all_done, 0)) *abort_flag = 1;
       __syncwarp();
+    } else if (warp > kMmaWarp && any) {
+      // ------------------------------------------------ a lane's segments
+      // one ahead of its softmax, which keeps its registers for scores; lane
+      // 0's warp also loads the segment's queries
+      const int i = warp - kMmaWarp - 1;
+      int ns = 0;
+      for (;; ++ns) {
+        if (lane == 0) segs[i * 2 + (ns & 1)] = sg;
+        if (i == 0) {
+          if (ns > 0) paged_wait(q_empty, (uint32_t)(ns - 1) & 1u, abort_flag);
+          if (lane == 0) {
+            const int tiles = min(tb, sg.s.n - sg.u * tb) * a.g > 128 ? 2 : 1;
+            const int y = (sg.head * a.total_q + sg.s.q0 + sg.u * tb) * a.g;
+            mbar_expect_tx(q_full, tiles * G::kTile);
+            for (int k = 0; k < tiles; ++k)
+              for (int h = 0; h < G::kHalves; ++h)
+                tma_load_2d(smem + k * G::kTile + h * G::kHalf, &tmQ, q_full, h * 64, y + k * 128);
+          }
+        }
+        __syncwarp();
+        bar_segment(i);
+        if (!next_segment<RB, KT>(a, pl, x1, sg)) break;
+      }
+      if (i == 0 && !mbar_wait(q_full, (uint32_t)ns & 1u)) *abort_flag = 1;  // landed, whatever happened
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
-    if (x0 < x1) {
+    if (any) {
       // ------------------------------------------------ softmax of lane `i`
-      const int i = warp >> 2, r = tid & 127;
-      const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      const int i = warp >> 3, hh = warp >> 2 & 1, q = warp & 3, r = 32 * q + lane;
+      const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
       const uint32_t tS = trow + i * 128, tO = trow + 256 + i * 128;
-      uint32_t cnt = 0;
-      int it = 0;
-      for (int64_t x = x0;;) {
-        const SeqInfo s = sg.s;
-        const int nt = sg.t1 - sg.t0, tok0 = sg.u * tb, live = min(tb, s.n - tok0) * a.g, nkeys = s.L + s.n;
+      uint8_t* slot = smem + G::kRowOff + (i * 128 + r) * 8;  // this row's two threads' words
+      __nv_bfloat16* half_max = reinterpret_cast<__nv_bfloat16*>(slot);  // [half]
+      uint32_t cnt = 0, nend = 0;  // this lane's tiles, and segments with tiles, so far
+      int it = 0, ns = 0;
+      for (;; ++ns) {
+        bar_segment(i);
+        const Segment& g = segs[i * 2 + (ns & 1)];
+        const int nt = g.t1 - g.t0, L = g.s.L, nkeys = L + g.s.n, tok0 = g.u * tb;
+        const int live = min(tb, g.s.n - tok0) * a.g;
         const bool wide = live > 128;
         const int row = wide ? i * 128 + r : r;
         const bool on = row < live;
-        const int tok = min(tok0 + row / a.g, s.n - 1);
-        const int lim = a.T ? nkeys : s.L + tok + 1;  // causal: keys below this
-        const uint32_t* anc = a.anc + (int64_t)tok * a.W;
+        const int tok = min(tok0 + row / a.g, g.s.n - 1);
+        const int key_base = g.t0 * KT;
+        // P is computed with the base of the tiles before while the tile's
+        // maximum is found; only where a row of the two warps passes its base by
+        // more than 8 (a segment's first tile, and seldom after) do they agree
+        // on new bases, rescale O and compute P again.
         float m = -INFINITY, l = 0.f;
         int done = 0;  // this lane's tiles of the segment
         for (int j = wide ? 0 : i; j < nt; j += wide ? 1 : 2, ++done) {
-          const int t = sg.t0 + j, key0 = t * KT;
+          const int key0 = key_base + j * KT + hh * 64;
           paged_wait(&s_full[i], cnt & 1u, abort_flag);
           __syncwarp();
           tc_fence_after();
-          uint32_t v[128];
+          uint32_t p[32];
+          float sum;
+          bool again = false;
+#pragma unroll 1
+          while (true) {
+            const float base = m == -INFINITY ? 0.f : m;
+            float mx[2] = {-INFINITY, -INFINITY}, sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
+            uint32_t v[2][32];
+            tmem_ld32(tS + hh * 64, v[0]);
+            tmem_ld_wait();
+            tmem_ld32(tS + hh * 64 + 32, v[1]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, v + c * 32);
-          tmem_ld_wait();
-          if (a.T == 0) {
-            if (__any_sync(0xffffffffu, lim < key0 + KT)) {
-              const int d = lim - key0;
+            for (int h = 0; h < 2; ++h) {  // 32 keys at a time
+              if (h == 1) tmem_ld_wait();
+              const int j0 = key0 + 32 * h;
+              if (a.T == 0) {
+                const int d = L + tok + 1 - j0;  // keys below this are seen
+                if (__any_sync(0xffffffffu, d < 32)) {
 #pragma unroll
-              for (int e = 0; e < 128; ++e) v[e] = e < d ? v[e] : 0xff800000u;
-            }
-          } else if (key0 + KT > s.L) {
+                  for (int e = 0; e < 32; ++e) v[h][e] = e < d ? v[h][e] : 0xff800000u;
+                }
+              } else if (j0 + 32 > L) {
+                const uint32_t* anc = a.anc + (int64_t)tok * a.W;
+                const int n0 = j0 - L;  // tree node of bit 0 (negative: prefix keys first)
+                uint32_t bits = 0xffffffffu;
+                if (n0 >= 0) {
+                  const int k = n0 >> 5, sh = n0 & 31;
+                  const uint32_t lo = k < a.W ? __ldg(anc + k) : 0u, hi = k + 1 < a.W ? __ldg(anc + k + 1) : 0u;
+                  bits = sh ? (lo >> sh) | (hi << (32 - sh)) : lo;
+                } else {
+                  bits = (0xffffffffu >> (32 + n0)) | (__ldg(anc) << (-n0));
+                }
+                const int past = nkeys - j0;  // nothing past the sequence
+                if (past < 32) bits &= past > 0 ? (1u << past) - 1u : 0u;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int j0 = key0 + 32 * w, n0 = j0 - s.L;  // tree node of bit 0 (negative: prefix keys first)
-              uint32_t bits = 0xffffffffu;
-              if (n0 >= 0) {
-                const int q = n0 >> 5, sh = n0 & 31;
-                const uint32_t lo = q < a.W ? __ldg(anc + q) : 0u, hi = q + 1 < a.W ? __ldg(anc + q + 1) : 0u;
-                bits = sh ? (lo >> sh) | (hi << (32 - sh)) : lo;
-              } else if (n0 > -32) {
-                bits = (0xffffffffu >> (32 + n0)) | (__ldg(anc) << (-n0));
+                for (int e = 0; e < 32; ++e) v[h][e] = (bits >> e & 1u) ? v[h][e] : 0xff800000u;
               }
-              const int past = nkeys - j0;  // nothing past the sequence
-              if (past < 32) bits &= past > 0 ? (1u << past) - 1u : 0u;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[32 * w + e] = (bits >> e & 1u) ? v[32 * w + e] : 0xff800000u;
+              for (int e = 0; e < 16; ++e) {
+                float u = __uint_as_float(v[h][2 * e]), w = __uint_as_float(v[h][2 * e + 1]);
+                mx[e & 1] = fmaxf(fmaxf(mx[e & 1], u), w);
+                add2(u, w, -base, -base);
+                u = ex2(u);
+                w = ex2(w);
+                add2(sa[e & 1], sb[e & 1], u, w);
+                p[h * 16 + e] = pack2_bf16(u, w);
+              }
             }
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < 128; e += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(v[e + 2 * k])), __uint_as_float(v[e + 2 * k + 1]));
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const bool far = mt > m + 8.f;
-          if (__any_sync(0xffffffffu, far)) {
-            const float mn = far ? mt : m;
-            const float al = m == -INFINITY ? 0.f : ex2(m - mn);
-            if (done > 0) {  // O so far holds what the old base gave
+            sum = (sa[0] + sb[0]) + (sa[1] + sb[1]);
+            if (again) {
+              bar_pair(i, q);  // both have read their scores: P may take their place
+              break;
+            }
+            const float mt = fmaxf(mx[0], mx[1]);
+            again = bar_pair_any(i, q, mt > m + 8.f);
+            if (!again) break;
+            // the base is a bf16 value: the row's threads tell each other their
+            // maxima rounded up, and any base near the maximum will do
+            const __nv_bfloat16 mine = __float2bfloat16_ru(mt);
+            half_max[hh] = mine;
+            bar_pair(i, q);
+            const float both = fmaxf(__bfloat162float(mine), __bfloat162float(half_max[hh ^ 1]));
+            const float mn = both > m + 8.f ? both : m;
+            // O so far holds what the old base gave; each thread has half of its
+            // columns.  This tile's scores say that the product before is done.
+            if (done > 0) {
+              const float al = m == -INFINITY ? 0.f : ex2(m - mn);
               l *= al;
-              paged_wait(&pv_done[i], (cnt - 1) & 1u, abort_flag);
-              __syncwarp();
-              tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < DH / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tO + c * 32, o);
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(tO + hh * (DH / 2) + c * 16, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                tmem_st32(tO + c * 32, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                tmem_st_32x32b_x16(tO + hh * (DH / 2) + c * 16, o);
               }
             }
             m = mn;
           }
-          const float base = m == -INFINITY ? 0.f : m;
-          float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t p[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float u = __uint_as_float(v[64 * h + 2 * e]), w = __uint_as_float(v[64 * h + 2 * e + 1]);
-              add2(u, w, -base, -base);
-              u = ex2(u);
-              w = ex2(w);
-              add2(sa[e & 1], sb[e & 1], u, w);
-              p[e] = pack2_bf16(u, w);
-            }
-            tmem_st32(tS + h * 32, p);
-          }
+          l += sum;
+          tmem_st_32x32b_x16(tS + hh * 32, p);
+          tmem_st_32x32b_x16(tS + hh * 32 + 16, p + 16);
           tmem_st_wait();
-          l += (sa[0] + sb[0]) + (sa[1] + sb[1]);
           // value rows past the sequence hold whatever the page does: zeros
           // (lane 0's P is waited for before either lane's product)
-          if (key0 + KT > nkeys && (i == 0 || !wide)) {
+          if (key_base + (j + 1) * KT > nkeys && (i == 0 || !wide)) {
             const int n = 2 * (it + j) + 1;
             paged_wait(&full[n % G::kSlots], (uint32_t)(n / G::kSlots) & 1u, abort_flag);
-            if (key0 + r >= nkeys) {
+            if (key_base + j * KT + r >= nkeys) {
 #pragma unroll
-              for (int c = 0; c < G::kHalves * 8; ++c)
-                *reinterpret_cast<uint4*>(smem + G::kRingOff + (n % G::kSlots) * G::kTile + (c >> 3) * G::kHalf +
-                                          r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+              for (int c = 0; c < G::kHalves * 4; ++c) {
+                const int ch = hh * G::kHalves * 4 + c;
+                *reinterpret_cast<uint4*>(smem + G::kRingOff + (n % G::kSlots) * G::kTile + (ch >> 3) * G::kHalf +
+                                          r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
             }
             fence_smem_async();
           }
           tc_fence_before();
-          mbar_arrive(&p_full[i]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[i]);
           ++cnt;
         }
+        // the row's sum from both halves
+        float* sums = reinterpret_cast<float*>(slot);
+        sums[hh] = l;
+        bar_pair(i, q);
+        l += sums[hh ^ 1];
+        bar_pair(i, q);  // both have read: the words are free again
         if (done > 0) {
-          paged_wait(&pv_done[i], (cnt - 1) & 1u, abort_flag);
+          paged_wait(&pv_done[i], nend & 1u, abort_flag);
+          ++nend;
           __syncwarp();
           tc_fence_after();
         }
-        // One query tile: the lanes' results are joined, half of the columns
-        // by each group (both read the same tensor-memory lanes).
-        int c0 = 0, c1 = DH / 32;
+        // Two query tiles: a thread ends with half of its row's columns.  One:
+        // the lanes' results are joined, and it has a quarter (all four threads
+        // read the same tensor-memory lane).
+        int c0 = hh * (DH / 2), c1 = c0 + DH / 2;
         float wa = 1.f, wb = 0.f;
         uint32_t ta = tO;
         const uint32_t tB = trow + 256 + 128;
         const bool two = !wide && nt > 1;
         if (!wide) {
-          xml[i * 128 + r] = make_float2(m, l);
+          if (hh == 0) {
+            sums[0] = l;
+            sums[1] = m;
+          }
           tc_fence_before();
-          bar_both();
+          bar_all();
           tc_fence_after();
-          const float2 e0 = xml[r], e1 = xml[128 + r];
-          m = fmaxf(e0.x, e1.x);
-          wa = e0.x == -INFINITY ? 0.f : ex2(e0.x - m);
-          wb = e1.x == -INFINITY ? 0.f : ex2(e1.x - m);
-          l = wa * e0.y + wb * e1.y;
+          const float2 e0 = *reinterpret_cast<const float2*>(smem + G::kRowOff + r * 8);
+          const float2 e1 = *reinterpret_cast<const float2*>(smem + G::kRowOff + (128 + r) * 8);
+          m = fmaxf(e0.y, e1.y);
+          wa = e0.y == -INFINITY ? 0.f : ex2(e0.y - m);
+          wb = e1.y == -INFINITY ? 0.f : ex2(e1.y - m);
+          l = wa * e0.x + wb * e1.x;
           ta = trow + 256;
-          c0 = i * (DH / 64);
-          c1 = c0 + DH / 64;
+          c0 = (i * 2 + hh) * (DH / 4);
+          c1 = c0 + DH / 4;
         }
-        auto columns = [&](int c, float* o) {  // columns 32c .. 32c+31 of the row
-          tmem_ld32(ta + c * 32, reinterpret_cast<uint32_t*>(o));
+        auto columns = [&](int c, float* o) {  // columns c .. c+15 of the row
+          tmem_ld_32x32b_x16(ta + c, reinterpret_cast<uint32_t*>(o));
           tmem_ld_wait();
           if (two) {
-            uint32_t u[32];
-            tmem_ld32(tB + c * 32, u);
+            uint32_t u[16];
+            tmem_ld_32x32b_x16(tB + c, u);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = o[e] * wa + __uint_as_float(u[e]) * wb;
+            for (int e = 0; e < 16; ++e) o[e] = o[e] * wa + __uint_as_float(u[e]) * wb;
           }
         };
+        uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                        ((int64_t)(g.s.q0 + tok) * a.H + (int64_t)g.head * a.g + row % a.g) * DH;
         auto put = [&](int c, const float* o, float inv) {
-          uint16_t* dst = static_cast<uint16_t*>(a.out) +
-                          ((int64_t)(s.q0 + tok) * a.H + (int64_t)sg.head * a.g + row % a.g) * DH + c * 32;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(dst + e * 8) =
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<uint4*>(dst + c + e * 8) =
                 make_uint4(pack2_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack2_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
                            pack2_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
                            pack2_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
         };
-        if (nt == sg.tiles) {
+        if (nt == g.tiles) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
-          for (int c = c0; c < c1; ++c) {
-            float o[32];
+          for (int c = c0; c < c1; c += 16) {
+            float o[16];
             columns(c, o);
             if (on) put(c, o, inv);
           }
           tc_fence_before();
-          if (!wide) bar_both();  // both groups have read both lanes
         } else {
           // a partial: four columns of a row in 16 bytes, rows side by side; then (m, l)
           int first, last;
-          unit_shares(sg, total, grid, first, last);
+          unit_shares(g, total, grid, first, last);
           const int pi = wide ? i : 0;
+          const int64_t unit_x = g.unit_x;
           auto part = [&](int c) {
-            return a.part + ((int64_t)part_slot(sg.unit_x, c, total, grid) * 2 + pi) * G::part_floats;
+            return a.part + ((int64_t)part_slot(unit_x, c, total, grid) * 2 + pi) * G::part_floats;
           };
           float* mine = part(blockIdx.x);
 #pragma unroll 1
-          for (int c = c0; c < c1; ++c) {
-            float o[32];
+          for (int c = c0; c < c1; c += 16) {
+            float o[16];
             columns(c, o);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 4; ++e)
               if (on)
-                *reinterpret_cast<float4*>(mine + ((c * 8 + e) * 128 + r) * 4) =
+                *reinterpret_cast<float4*>(mine + ((c / 4 + e) * 128 + r) * 4) =
                     make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           tc_fence_before();
-          if (wide || i == 0) *reinterpret_cast<float2*>(mine + 128 * DH + 2 * r) = make_float2(m, l);
-          if (wide) bar_group(i); else bar_both();
-          if (r == 0 && pi == i) {
+          if (hh == 0 && pi == i) *reinterpret_cast<float2*>(mine + 128 * DH + 2 * r) = make_float2(m, l);
+          if (wide) bar_lane(i); else bar_all();
+          if (r == 0 && hh == 0 && pi == i) {
             const int before = arrive_acq_rel(a.counters + first * 2 + i);
             s_flag[i] = before == last - first;
             if (before == last - first) a.counters[first * 2 + i] = 0;  // ready for the next call
           }
-          if (wide) bar_group(i); else bar_both();
+          if (wide) bar_lane(i); else bar_all();
           if (s_flag[pi] && on) {
             float M = -INFINITY, sum = 0.f;
             for (int c = first; c <= last; ++c) {
@@ -522,18 +676,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
-            for (int c = c0; c < c1; ++c) {
-              float acc[32];
+            for (int c = c0; c < c1; c += 16) {
+              float acc[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+              for (int e = 0; e < 16; ++e) acc[e] = 0.f;
               for (int k = first; k <= last; ++k) {
                 const float* pt = part(k);
                 const float pm = __ldcg(pt + 128 * DH + 2 * r);
                 if (pm == -INFINITY) continue;
                 const float w = ex2(pm - M);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float4 f = __ldcg(reinterpret_cast<const float4*>(pt + ((c * 8 + e) * 128 + r) * 4));
+                for (int e = 0; e < 4; ++e) {
+                  const float4 f = __ldcg(reinterpret_cast<const float4*>(pt + ((c / 4 + e) * 128 + r) * 4));
                   acc[4 * e] += w * f.x;
                   acc[4 * e + 1] += w * f.y;
                   acc[4 * e + 2] += w * f.z;
@@ -545,16 +699,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
+        if (!wide) bar_all();  // everyone has read both lanes and the rows' words
         it += nt;
-        x += nt;
-        if (x >= x1) break;
-        next_segment<RB, KT>(a, pl, x, x1, sg);
+        // another unit with a tile before x1?
+        if (g.unit_x + g.tiles + kUnitCost + kUnitCost >= x1) break;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }

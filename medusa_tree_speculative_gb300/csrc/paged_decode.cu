@@ -127,9 +127,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   make_plan<kThreads, RB, KT>(a, sc, pl, x0, x1);
   const int64_t total = pl.total, grid = min((int64_t)gridDim.x, total);
   Segment sg;
-  if (x0 < x1) seek_segment<RB, KT>(a, sc, x0, x1, sg);
+  const bool any = x0 < x1 && seek_segment<RB, KT>(a, sc, x0, x1, sg);
   __syncthreads();  // the scratch becomes the warps' results
-  if (x0 < x1) {
+  if (any) {
     if (warp == 4) {
       // ------------------------------------------------ loads
       const int box = min(a.p.page_size, KT), runs = KT / box;  // runs of keys in one page each
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap* map = op_v ? &tmV : &tmK;
       bool told = false;
       int it = 0;
-      for (int64_t x = x0;;) {
+      while (true) {
         const SeqInfo& s = sg.s;
         const int nkeys = s.L + s.n;
         for (int t = sg.t0; t < sg.t1; ++t, ++it) {
@@ -162,9 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d(smem + st * 2 * G::kTile + op_v * G::kTile + op_half * G::kHalf + op_run * box * 128, map,
                         &full[st], op_half * 64, y);
         }
-        x += sg.t1 - sg.t0;
-        if (x >= x1) break;
-        next_segment<RB, KT>(a, pl, x, x1, sg);
+        if (!next_segment<RB, KT>(a, pl, x1, sg)) break;
       }
       // the copies in flight land before the CTA can end, whatever happened
       for (int j = max(0, it - G::kStages); j < it; ++j)
@@ -172,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 5) {
       // ------------------------------------------------ queries
       int n = 0;
-      for (int64_t x = x0;; ++n) {
+      for (;; ++n) {
         const int bf = n & 1;
         const int live = sg.s.n * a.g;
         paged_wait(&q_empty[bf], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag);
@@ -201,27 +199,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) segs[bf] = sg;
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[bf]);
-        x += sg.t1 - sg.t0;
-        if (x >= x1) break;
-        next_segment<RB, KT>(a, pl, x, x1, sg);
+        if (!next_segment<RB, KT>(a, pl, x1, sg)) break;
       }
     } else {
       // ------------------------------------------------ append, then attend
+      int segments;
       {
         int n = 0;
         Segment g = sg;
-        for (int64_t x = x0;; ++n) {  // segments in turn to the four warps
-          if ((n & 3) == warp && g.t1 * KT > g.s.L) append_tokens<DH>(a, g, lane);
-          x += g.t1 - g.t0;
-          if (x >= x1) break;
-          next_segment<RB, KT>(a, pl, x, x1, g);
-        }
+        do {  // segments in turn to the four warps
+          if ((n++ & 3) == warp && g.t1 * KT > g.s.L) append_tokens<DH>(a, g, lane);
+        } while (next_segment<RB, KT>(a, pl, x1, g));
+        segments = n;
         asm volatile("fence.proxy.async.global;\n" ::: "memory");  // the tiles' loads read them back
         mbar_arrive(appended);
       }
       const int r0 = lane >> 2, r1 = r0 + 8, kc = (lane & 3) * 2;  // this thread's rows and key columns
-      int it = 0, n = 0;
-      for (int64_t x = x0; x < x1; ++n) {
+      int it = 0;
+      for (int n = 0; n < segments; ++n) {
         const int bf = n & 1;
         paged_wait(&q_full[bf], (uint32_t)(n >> 1) & 1u, abort_flag);
         const Segment g = segs[bf];
@@ -424,7 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             put();
           }
         }
-        x += g.t1 - g.t0;
       }
     }
   }
