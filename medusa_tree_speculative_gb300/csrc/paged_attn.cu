@@ -149,11 +149,11 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
   int* flag = reinterpret_cast<int*>(&pl + 1);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   int64_t x, x1;
-  make_plan<kGenThreads, RB, KT>(a, sc, pl, x, x1);
+  make_plan<kGenThreads, RB, KT, 1>(a, sc, pl, x, x1);
   const int64_t total = pl.total, grid = min((int64_t)gridDim.x, total);
   const int tb = RB / a.g;
   Segment sg;
-  if (x >= x1 || !seek_segment<RB, KT>(a, sc, x, x1, sg)) return;
+  if (x >= x1 || !seek_segment<RB, KT, 1>(a, sc, x, x1, sg)) return;
   while (true) {
     const SeqInfo& s = sg.s;
     const int nkeys = s.L + s.n, tok0 = sg.u * tb, live = min(tb, s.n - tok0) * a.g;
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
       for (int i = 0; i < G::TM; ++i) put(i, o[i], l[i]);
     } else {
       int first, last;
-      unit_shares(sg, total, grid, first, last);
+      unit_shares<1>(sg, total, grid, first, last);
       float* mine = a.part + (int64_t)part_slot(sg.unit_x, blockIdx.x, total, grid) * G::part_floats;
 #pragma unroll
       for (int i = 0; i < G::TM; ++i) {
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
         }
       }
     }
-    if (!next_segment<RB, KT>(a, pl, x1, sg)) break;
+    if (!next_segment<RB, KT, 1>(a, pl, x1, sg)) break;
   }
 }
 

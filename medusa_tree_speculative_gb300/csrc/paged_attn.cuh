@@ -6,7 +6,7 @@
 // tokens (RB / g of them), so that one pass over the keys serves all g heads.
 // A unit reads the key tiles its last token sees.  All units' tiles, in the
 // order (sequence, key head, block, tile), form one list, in which each unit
-// also has kUnitCost empty places before its first tile, for the time that
+// also has `EC` empty places before its first tile, for the time that
 // beginning and ending a unit takes.  The grid's CTAs share the list's N
 // places out evenly: CTA c of G takes [c N / G, (c + 1) N / G).  So ragged
 // batches, one long sequence and a causal triangle are balanced alike, and
@@ -32,7 +32,6 @@ namespace medusa {
 constexpr int kPagedMaxGroup = 64;     // query heads per key head
 constexpr int kFewRows = 16;           // rows (tokens x heads of a key head) of the kernels for few rows
 constexpr int kPagedCounters = 1024;   // arrival counters of one kernel
-constexpr int kUnitCost = 2;           // places in the list of work that a unit has besides its tiles
 constexpr float kPagedLog2e = 1.4426950408889634f;
 
 struct PagedAttnArgs {
@@ -93,15 +92,15 @@ MDEV int unit_tiles(const PagedAttnArgs& a, const SeqInfo& s, int tb, int u) {
   const int seen = a.T ? s.n : min(s.n, (u + 1) * tb);
   return (s.L + seen + KT - 1) / KT;
 }
-// Places of blocks 0 .. u-1, all of them full: u kUnitCost and the sum over i of
+// Places of blocks 0 .. u-1, all of them full: u EC and the sum over i of
 // floor((L + (i + 1) tb + KT - 1) / KT), by Euclid's reduction of the sum of
 // floor((A i + C) / M) (lattice points below a line).
-template <int KT>
+template <int KT, int EC>
 MDEV int64_t places_before(const PagedAttnArgs& a, const SeqInfo& s, int tb, int u) {
   if (u <= 0) return 0;
-  if (a.T) return (int64_t)u * ((s.L + s.n + KT - 1) / KT + kUnitCost);
+  if (a.T) return (int64_t)u * ((s.L + s.n + KT - 1) / KT + EC);
   uint64_t n = (uint64_t)u, m = KT, x = (uint64_t)tb, c = (uint64_t)s.L + tb + KT - 1;
-  int64_t sum = (int64_t)u * kUnitCost;
+  int64_t sum = (int64_t)u * EC;
   while (true) {
     sum += (int64_t)((n - 1) * n / 2 * (x / m));
     x %= m;
@@ -118,10 +117,10 @@ MDEV int64_t places_before(const PagedAttnArgs& a, const SeqInfo& s, int tb, int
   return sum;
 }
 // Places of one key head of a sequence.
-template <int KT>
+template <int KT, int EC>
 MDEV int64_t seq_places(const PagedAttnArgs& a, const SeqInfo& s, int tb) {
   const int m = (s.n + tb - 1) / tb;
-  return places_before<KT>(a, s, tb, m - 1) + kUnitCost + unit_tiles<KT>(a, s, tb, m - 1);
+  return places_before<KT, EC>(a, s, tb, m - 1) + EC + unit_tiles<KT>(a, s, tb, m - 1);
 }
 
 // Shared memory for the plan: scratch, used only while it is made, and what
@@ -145,7 +144,7 @@ struct Segment {
 };
 
 // Build the plan (all NT threads of the CTA); x0, x1: this CTA's places.
-template <int NT, int RB, int KT>
+template <int NT, int RB, int KT, int EC>
 MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& x0, int64_t& x1) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int tb = RB / a.g;
@@ -177,7 +176,7 @@ MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& 
     sc.pre[b] = mine;
     if (ok) {
       atomicOr(&pl.valid[b >> 5], 1u << (b & 31));
-      mine += (int64_t)a.Hkv * seq_places<KT>(a, s, tb);
+      mine += (int64_t)a.Hkv * seq_places<KT, EC>(a, s, tb);
     }
   }
   int64_t x = mine;
@@ -214,8 +213,9 @@ MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& 
 }
 
 // The tiles of unit g in places [x, x1) of the list; false if there are none.
+template <int EC>
 MDEV bool set_tiles(Segment& g, int64_t x, int64_t x1) {
-  const int64_t tile0 = g.unit_x + kUnitCost;
+  const int64_t tile0 = g.unit_x + EC;
   g.t0 = (int)max((int64_t)0, x - tile0);
   g.t1 = (int)min((int64_t)g.tiles, x1 - tile0);
   return g.t0 < g.t1;
@@ -223,7 +223,7 @@ MDEV bool set_tiles(Segment& g, int64_t x, int64_t x1) {
 
 // The segment that place x of the list is in (x < x1); false if [x, x1) has no
 // tiles.
-template <int RB, int KT>
+template <int RB, int KT, int EC>
 MDEV bool seek_segment(const PagedAttnArgs& a, const PlanScratch& sc, int64_t x, int64_t x1, Segment& g) {
   const int tb = RB / a.g;
   int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before x: it has places, or total would be x
@@ -235,27 +235,27 @@ MDEV bool seek_segment(const PagedAttnArgs& a, const PlanScratch& sc, int64_t x,
   int code;
   seq_info(a, lo, g.s, code);
   g.m = (g.s.n + tb - 1) / tb;
-  const int64_t each = seq_places<KT>(a, g.s, tb);
+  const int64_t each = seq_places<KT, EC>(a, g.s, tb);
   int64_t rest = x - sc.pre[lo];
   g.head = (int)(rest / each);
   rest -= (int64_t)g.head * each;
   int ulo = 0, uhi = g.m - 1;
   while (ulo < uhi) {
     const int mid = (ulo + uhi + 1) >> 1;
-    if (places_before<KT>(a, g.s, tb, mid) <= rest) ulo = mid; else uhi = mid - 1;
+    if (places_before<KT, EC>(a, g.s, tb, mid) <= rest) ulo = mid; else uhi = mid - 1;
   }
   g.u = ulo;
-  rest -= places_before<KT>(a, g.s, tb, ulo);
+  rest -= places_before<KT, EC>(a, g.s, tb, ulo);
   g.tiles = unit_tiles<KT>(a, g.s, tb, ulo);
   g.unit_x = x - rest;
-  return set_tiles(g, x, x1);
+  return set_tiles<EC>(g, x, x1);
 }
 
 // The segment after g; false if this CTA's places before x1 have none.
-template <int RB, int KT>
+template <int RB, int KT, int EC>
 MDEV bool next_segment(const PagedAttnArgs& a, const Plan& pl, int64_t x1, Segment& g) {
   const int tb = RB / a.g;
-  g.unit_x += g.tiles + kUnitCost;
+  g.unit_x += g.tiles + EC;
   if (g.unit_x >= x1) return false;
   if (++g.u == g.m) {
     g.u = 0;
@@ -269,16 +269,17 @@ MDEV bool next_segment(const PagedAttnArgs& a, const Plan& pl, int64_t x1, Segme
     }
   }
   g.tiles = unit_tiles<KT>(a, g.s, tb, g.u);
-  return set_tiles(g, g.unit_x, x1);
+  return set_tiles<EC>(g, g.unit_x, x1);
 }
 
 // CTA that holds place x of the list.
 MDEV int cta_of(int64_t x, int64_t total, int64_t G) { return (int)(((x + 1) * G - 1) / total); }
 
 // Who shares the unit of g: its first and last CTA.
+template <int EC>
 MDEV void unit_shares(const Segment& g, int64_t total, int64_t G, int& first, int& last) {
-  first = cta_of(g.unit_x + kUnitCost, total, G);
-  last = cta_of(g.unit_x + kUnitCost + g.tiles - 1, total, G);
+  first = cta_of(g.unit_x + EC, total, G);
+  last = cta_of(g.unit_x + EC + g.tiles - 1, total, G);
 }
 // Slot (of two) of CTA c's partial of the unit that starts at unit_x: 0 if it
 // is the CTA's first segment, else 1 (a CTA that starts in an earlier unit has

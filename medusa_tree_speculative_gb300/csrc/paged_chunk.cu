@@ -39,6 +39,7 @@ namespace {
 using namespace sm100;
 
 constexpr int RB = 256, KT = 128;
+constexpr int kCost = 3;  // 8192 tokens: 535, 502, 486, 489 us at 1, 2, 3, 4
 constexpr int kThreads = 640;  // two softmax groups of 256; the load warp, the MMA warp and two segment warps
 constexpr int kSoft = 512, kLoadWarp = 16, kMmaWarp = 17;
 // Registers: the block starts with 96 a thread (640 x 96 = 61440); the softmax
@@ -46,11 +47,6 @@ constexpr int kSoft = 512, kLoadWarp = 16, kMmaWarp = 17;
 constexpr int kLaunchRegs = 96, kSoftRegs = 104, kOtherRegs = 64;
 static_assert(kSoft * kSoftRegs + (kThreads - kSoft) * kOtherRegs <= kThreads * kLaunchRegs, "registers");
 constexpr uint32_t kTmemCols = 512;
-
-template <uint32_t B>
-struct Half {
-  static constexpr uint32_t value = B;
-};
 
 template <int DH>
 struct Cfg {
@@ -214,10 +210,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   int64_t x0, x1;
-  make_plan<kThreads, RB, KT>(a, sc, pl, x0, x1);
+  make_plan<kThreads, RB, KT, kCost>(a, sc, pl, x0, x1);
   const int64_t total = pl.total, grid = min((int64_t)gridDim.x, total);
   Segment sg;
-  const bool any = x0 < x1 && seek_segment<RB, KT>(a, sc, x0, x1, sg);
+  const bool any = x0 < x1 && seek_segment<RB, KT, kCost>(a, sc, x0, x1, sg);
   fence_smem_async();  // the scratch was read and written; the ring's copies follow
   tc_fence_before();
   __syncthreads();
@@ -256,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           kv ? &tmV : &tmK, &full[sl], op_half * 64, y);
           }
         }
-        if (!next_segment<RB, KT>(a, pl, x1, sg)) break;
+        if (!next_segment<RB, KT, kCost>(a, pl, x1, sg)) break;
       }
       // the copies in flight land before the CTA can end, whatever happened
       for (int j = max(0, n - G::kSlots); j < n; ++j)
@@ -302,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ready = false;  // the segment's first scores are on their way
       while (true) {
         const uint32_t n = nt, w = wide;
-        const uint32_t more = uni(next_segment<RB, KT>(a, pl, x1, sg));
+        const uint32_t more = uni(next_segment<RB, KT, kCost>(a, pl, x1, sg));
         if (more) enter();
         const bool chain = more && w && wide;  // the next segment's first scores follow this one's last
         if (!ready) {
@@ -326,52 +322,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (w) {
-          // tile t in ring half b: PV0, QK0 of the next, PV1, QK1 of the next
-          auto tile = [&](auto half, uint32_t j) {
-            constexpr uint32_t b = decltype(half)::value;
-            const bool end = j + 1 == n, go = !end || chain, qe = j + 2 == n || (end && chain && nt == 1);
+          // PV0(j), QK0(j + 1), PV1(j), QK1(j + 1): one copy of the code for both
+          // lanes and ring halves (unrolled by them it was 5% slower: the
+          // instruction cache also holds the softmax)
+          for (uint32_t j = 0; j < n; ++j, ++t) {
+            const uint32_t b = uni(t & 1u), end = uni(j + 1 == n), go = uni(!end || chain);
+            const uint32_t qe = uni(j + 2 == n || (end && chain && nt == 1));
             wait_at(bars + b * 16 + 8, t >> 1 & 1u, abort_flag);  // ahead of P
-            wait_at(bars + kP, ph0, abort_flag);
-            tc_fence_after();
-            if (elect_one()) {
-              pv(0, v16 + b * 2 * kTile16, j > 0);
-              if (end) commit_at(bars + kPV);
-            }
-            __syncwarp();
-            if (go) {
-              if (end) {
-                wait_at(bars + kQ, qph, abort_flag);
-                qph ^= 1u;
-              }
-              wait_at(bars + (b ^ 1) * 16, (t + 1) >> 1 & 1u, abort_flag);
+#pragma unroll 1
+            for (uint32_t i = 0; i < 2; ++i) {
+              wait_at(bars + kP + i * 8, i ? ph1 : ph0, abort_flag);
               tc_fence_after();
               if (elect_one()) {
-                qk(0, q16, k16 + (b ^ 1) * 2 * kTile16);
-                commit_at(bars + kS);
+                pv(i * 128, v16 + b * 2 * kTile16, j > 0);
+                if (i) commit_at(bars + kEmpty + b * 16 + 8);
+                if (end) commit_at(bars + kPV + i * 8);
               }
               __syncwarp();
-            }
-            wait_at(bars + kP + 8, ph1, abort_flag);
-            tc_fence_after();
-            if (elect_one()) {
-              pv(128, v16 + b * 2 * kTile16, j > 0);
-              commit_at(bars + kEmpty + b * 16 + 8);
-              if (end) commit_at(bars + kPV + 8);
               if (go) {
-                qk(128, q16 + kTile16, k16 + (b ^ 1) * 2 * kTile16);
-                commit_at(bars + kS + 8);
-                commit_at(bars + kEmpty + (b ^ 1) * 16);
-                if (qe) commit_at(bars + kQE);
+                if (i == 0) {
+                  if (end) {
+                    wait_at(bars + kQ, qph, abort_flag);
+                    qph ^= 1u;
+                  }
+                  wait_at(bars + (b ^ 1) * 16, (t + 1) >> 1 & 1u, abort_flag);
+                  tc_fence_after();
+                }
+                if (elect_one()) {
+                  qk(i * 128, q16 + i * kTile16, k16 + (b ^ 1) * 2 * kTile16);
+                  commit_at(bars + kS + i * 8);
+                  if (i) commit_at(bars + kEmpty + (b ^ 1) * 16);
+                  if (i && qe) commit_at(bars + kQE);
+                }
+                __syncwarp();
               }
             }
-            __syncwarp();
             ph0 ^= 1u;
             ph1 ^= 1u;
-            ++t;
-          };
-          for (uint32_t j = 0; j < n; ++j) {
-            if (t & 1u) tile(Half<1>(), j);
-            else tile(Half<0>(), j);
           }
           ready = chain;
         } else {
@@ -429,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         bar_segment(i);
-        if (!next_segment<RB, KT>(a, pl, x1, sg)) break;
+        if (!next_segment<RB, KT, kCost>(a, pl, x1, sg)) break;
       }
       if (i == 0 && !mbar_wait(q_full, (uint32_t)ns & 1u)) *abort_flag = 1;  // landed, whatever happened
     }
@@ -640,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // a partial: four columns of a row in 16 bytes, rows side by side; then (m, l)
           int first, last;
-          unit_shares(g, total, grid, first, last);
+          unit_shares<kCost>(g, total, grid, first, last);
           const int pi = wide ? i : 0;
           const int64_t unit_x = g.unit_x;
           auto part = [&](int c) {
@@ -702,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wide) bar_all();  // everyone has read both lanes and the rows' words
         it += nt;
         // another unit with a tile before x1?
-        if (g.unit_x + g.tiles + kUnitCost + kUnitCost >= x1) break;
+        if (g.unit_x + g.tiles + 2 * kCost >= x1) break;
       }
     }
   }

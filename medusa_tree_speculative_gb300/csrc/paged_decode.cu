@@ -29,7 +29,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int RB = 16, KT = 64;
+constexpr int RB = 16, KT = 64, kCost = 2;
 constexpr int kThreads = 192;
 constexpr int kConsumers = 128;
 
@@ -124,10 +124,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // rows past a segment's own keep whatever was here before: finite numbers
   for (uint32_t e = tid; e < G::kQBytes / 4; e += kThreads) reinterpret_cast<uint32_t*>(smem + G::kQOff)[e] = 0u;
   int64_t x0, x1;
-  make_plan<kThreads, RB, KT>(a, sc, pl, x0, x1);
+  make_plan<kThreads, RB, KT, kCost>(a, sc, pl, x0, x1);
   const int64_t total = pl.total, grid = min((int64_t)gridDim.x, total);
   Segment sg;
-  const bool any = x0 < x1 && seek_segment<RB, KT>(a, sc, x0, x1, sg);
+  const bool any = x0 < x1 && seek_segment<RB, KT, kCost>(a, sc, x0, x1, sg);
   __syncthreads();  // the scratch becomes the warps' results
   if (any) {
     if (warp == 4) {
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d(smem + st * 2 * G::kTile + op_v * G::kTile + op_half * G::kHalf + op_run * box * 128, map,
                         &full[st], op_half * 64, y);
         }
-        if (!next_segment<RB, KT>(a, pl, x1, sg)) break;
+        if (!next_segment<RB, KT, kCost>(a, pl, x1, sg)) break;
       }
       // the copies in flight land before the CTA can end, whatever happened
       for (int j = max(0, it - G::kStages); j < it; ++j)
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) segs[bf] = sg;
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[bf]);
-        if (!next_segment<RB, KT>(a, pl, x1, sg)) break;
+        if (!next_segment<RB, KT, kCost>(a, pl, x1, sg)) break;
       }
     } else {
       // ------------------------------------------------ append, then attend
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Segment g = sg;
         do {  // segments in turn to the four warps
           if ((n++ & 3) == warp && g.t1 * KT > g.s.L) append_tokens<DH>(a, g, lane);
-        } while (next_segment<RB, KT>(a, pl, x1, g));
+        } while (next_segment<RB, KT, kCost>(a, pl, x1, g));
         segments = n;
         asm volatile("fence.proxy.async.global;\n" ::: "memory");  // the tiles' loads read them back
         mbar_arrive(appended);
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           put();
         } else {
           int first, last;
-          unit_shares(g, total, grid, first, last);
+          unit_shares<kCost>(g, total, grid, first, last);
           float* mine = a.part + (int64_t)part_slot(g.unit_x, blockIdx.x, total, grid) * G::part_floats;
           if (r < live) {
 #pragma unroll
