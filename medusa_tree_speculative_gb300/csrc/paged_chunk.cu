@@ -9,12 +9,12 @@
 // thread's order is PV0(j), QK0(j+1), PV1(j), QK1(j+1), ..., so a lane's
 // softmax has the other lane's two products, 1024 cycles, to hide behind.  The
 // kernel is bound by the tensor core where that holds.
-//   * warps 0-7 and 8-15 are the lanes' softmax, two threads per query row
-//     (its tensor-memory lane), one per half of the tile's keys: each reads 64
-//     scores, the two agree on the row's maximum through shared memory, and
-//     write P = 2^(S - m) in bf16 over the scores in tensor memory.  One thread
-//     per row took 1700 cycles from scores to P, 660 more than the other
-//     lane's products hide.
+//   * warps 0-3 and 4-7 are the lanes' softmax: a thread per query row (its
+//     tensor-memory lane) reads 128 scores and writes P = 2^(S - m) in bf16
+//     over them in tensor memory, with no exchange between threads.  (Two
+//     threads per row, which agree on the maximum through shared memory, take
+//     less time from scores to P, but issue 1.7 times the instructions, and the
+//     MMA warp shares the issue slots: 466 us against 448 for 8192 tokens.)
 //   * O stays in tensor memory.  The base m of a row only moves when the
 //     row's maximum passes it by more than 8 (P is at most 2^8, its sum is
 //     kept in 32 bits), so O is rescaled a few times per row and not per tile.
@@ -40,11 +40,12 @@ using namespace sm100;
 
 constexpr int RB = 256, KT = 128;
 constexpr int kCost = 3;  // 8192 tokens: 535, 502, 486, 489 us at 1, 2, 3, 4
-constexpr int kThreads = 640;  // two softmax groups of 256; the load warp, the MMA warp and two segment warps
-constexpr int kSoft = 512, kLoadWarp = 16, kMmaWarp = 17;
-// Registers: the block starts with 96 a thread (640 x 96 = 61440); the softmax
-// threads then take what the other warps give up: 512 x 104 + 128 x 64.
-constexpr int kLaunchRegs = 96, kSoftRegs = 104, kOtherRegs = 64;
+constexpr int kThreads = 384;  // two softmax groups of 128; the load warp, the MMA warp and two segment warps
+constexpr int kSoft = 256, kLoadWarp = 8, kMmaWarp = 9;
+// Registers: the block starts with 168 a thread (384 x 168 = 64512); the softmax
+// threads, which hold 128 scores, then take what the other warps give up:
+// 256 x 208 + 128 x 88.
+constexpr int kLaunchRegs = 168, kSoftRegs = 208, kOtherRegs = 88;
 static_assert(kSoft * kSoftRegs + (kThreads - kSoft) * kOtherRegs <= kThreads * kLaunchRegs, "registers");
 constexpr uint32_t kTmemCols = 512;
 
@@ -79,21 +80,11 @@ MDEV bool elect_one() {
   return p != 0;
 }
 MDEV void fence_smem_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
-// Barriers of a row quarter's two warps, of a lane's 256 threads, of all 512.
-MDEV void bar_pair(int i, int q) { asm volatile("bar.sync %0, 64;\n" ::"r"(1 + i * 4 + q) : "memory"); }
-MDEV bool bar_pair_any(int i, int q, bool flag) {
-  int any;
-  asm volatile(
-      "{\n\t.reg .pred f, r;\n\tsetp.ne.s32 f, %1, 0;\n\tbarrier.red.or.pred r, %2, 64, f;\n\tselp.s32 %0, 1, 0, r;\n\t}\n"
-      : "=r"(any)
-      : "r"((int)flag), "r"(1 + i * 4 + q)
-      : "memory");
-  return any != 0;
-}
-MDEV void bar_lane(int i) { asm volatile("bar.sync %0, 256;\n" ::"r"(9 + i) : "memory"); }
-// A lane's threads and the warp that writes its segments.
-MDEV void bar_segment(int i) { asm volatile("bar.sync %0, 288;\n" ::"r"(12 + i) : "memory"); }
-MDEV void bar_all() { asm volatile("bar.sync 11, 512;\n" ::: "memory"); }
+// Barriers of a lane's threads and the warp that writes its segments, of a
+// lane's 128 threads, of all 256.
+MDEV void bar_segment(int i) { asm volatile("bar.sync %0, 160;\n" ::"r"(1 + i) : "memory"); }
+MDEV void bar_lane(int i) { asm volatile("bar.sync %0, 128;\n" ::"r"(3 + i) : "memory"); }
+MDEV void bar_all() { asm volatile("bar.sync 5, 256;\n" ::: "memory"); }
 MDEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -193,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 8);
+      mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(q_full, 1);
@@ -424,11 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
     if (any) {
       // ------------------------------------------------ softmax of lane `i`
-      const int i = warp >> 3, hh = warp >> 2 & 1, q = warp & 3, r = 32 * q + lane;
+      const int i = warp >> 2, q = warp & 3, r = 32 * q + lane;
       const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
       const uint32_t tS = trow + i * 128, tO = trow + 256 + i * 128;
-      uint8_t* slot = smem + G::kRowOff + (i * 128 + r) * 8;  // this row's two threads' words
-      __nv_bfloat16* half_max = reinterpret_cast<__nv_bfloat16*>(slot);  // [half]
+      float2* row_ml = reinterpret_cast<float2*>(smem + G::kRowOff);  // [2 lanes][128 rows] (max, sum)
       uint32_t cnt = 0, nend = 0;  // this lane's tiles, and segments with tiles, so far
       int it = 0, ns = 0;
       for (;; ++ns) {
@@ -441,100 +431,97 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool on = row < live;
         const int tok = min(tok0 + row / a.g, g.s.n - 1);
         const int key_base = g.t0 * KT;
-        // P is computed with the base of the tiles before while the tile's
-        // maximum is found; only where a row of the two warps passes its base by
-        // more than 8 (a segment's first tile, and seldom after) do they agree
-        // on new bases, rescale O and compute P again.
         float m = -INFINITY, l = 0.f;
         int done = 0;  // this lane's tiles of the segment
         for (int j = wide ? 0 : i; j < nt; j += wide ? 1 : 2, ++done) {
-          const int key0 = key_base + j * KT + hh * 64;
+          const int key0 = key_base + j * KT;
           paged_wait(&s_full[i], cnt & 1u, abort_flag);
           __syncwarp();
           tc_fence_after();
-          uint32_t p[32];
-          float sum;
-          bool again = false;
-#pragma unroll 1
-          while (true) {
-            const float base = m == -INFINITY ? 0.f : m;
-            float mx[2] = {-INFINITY, -INFINITY}, sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
-            uint32_t v[2][32];
-            tmem_ld32(tS + hh * 64, v[0]);
-            tmem_ld_wait();
-            tmem_ld32(tS + hh * 64 + 32, v[1]);
+          uint32_t v[128];
+          tmem_ld32(tS, v);
+          tmem_ld32(tS + 32, v + 32);
+          tmem_ld_wait();
+          tmem_ld32(tS + 64, v + 64);
+          tmem_ld32(tS + 96, v + 96);
+          auto mask = [&](int c0) {  // keys c0 .. c0 + 63 of the tile
+            if (a.T == 0) {
+              const int d = L + tok + 1 - key0;  // keys below this are seen
+              if (__any_sync(0xffffffffu, d < c0 + 64)) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 32 keys at a time
-              if (h == 1) tmem_ld_wait();
-              const int j0 = key0 + 32 * h;
-              if (a.T == 0) {
-                const int d = L + tok + 1 - j0;  // keys below this are seen
-                if (__any_sync(0xffffffffu, d < 32)) {
+                for (int e = 0; e < 64; ++e) v[c0 + e] = c0 + e < d ? v[c0 + e] : 0xff800000u;
+              }
+            } else if (key0 + c0 + 64 > L) {
+              const uint32_t* anc = a.anc + (int64_t)tok * a.W;
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) v[h][e] = e < d ? v[h][e] : 0xff800000u;
-                }
-              } else if (j0 + 32 > L) {
-                const uint32_t* anc = a.anc + (int64_t)tok * a.W;
-                const int n0 = j0 - L;  // tree node of bit 0 (negative: prefix keys first)
+              for (int w = 0; w < 2; ++w) {
+                const int j0 = key0 + c0 + 32 * w, n0 = j0 - L;  // tree node of bit 0 (negative: prefix keys first)
                 uint32_t bits = 0xffffffffu;
                 if (n0 >= 0) {
                   const int k = n0 >> 5, sh = n0 & 31;
                   const uint32_t lo = k < a.W ? __ldg(anc + k) : 0u, hi = k + 1 < a.W ? __ldg(anc + k + 1) : 0u;
                   bits = sh ? (lo >> sh) | (hi << (32 - sh)) : lo;
-                } else {
+                } else if (n0 > -32) {
                   bits = (0xffffffffu >> (32 + n0)) | (__ldg(anc) << (-n0));
                 }
                 const int past = nkeys - j0;  // nothing past the sequence
                 if (past < 32) bits &= past > 0 ? (1u << past) - 1u : 0u;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[h][e] = (bits >> e & 1u) ? v[h][e] : 0xff800000u;
+                for (int e = 0; e < 32; ++e) v[c0 + 32 * w + e] = (bits >> e & 1u) ? v[c0 + 32 * w + e] : 0xff800000u;
               }
+            }
+          };
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto maxima = [&](int c0) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float u = __uint_as_float(v[h][2 * e]), w = __uint_as_float(v[h][2 * e + 1]);
-                mx[e & 1] = fmaxf(fmaxf(mx[e & 1], u), w);
-                add2(u, w, -base, -base);
-                u = ex2(u);
-                w = ex2(w);
-                add2(sa[e & 1], sb[e & 1], u, w);
-                p[h * 16 + e] = pack2_bf16(u, w);
-              }
-            }
-            sum = (sa[0] + sb[0]) + (sa[1] + sb[1]);
-            if (again) {
-              bar_pair(i, q);  // both have read their scores: P may take their place
-              break;
-            }
-            const float mt = fmaxf(mx[0], mx[1]);
-            again = bar_pair_any(i, q, mt > m + 8.f);
-            if (!again) break;
-            // the base is a bf16 value: the row's threads tell each other their
-            // maxima rounded up, and any base near the maximum will do
-            const __nv_bfloat16 mine = __float2bfloat16_ru(mt);
-            half_max[hh] = mine;
-            bar_pair(i, q);
-            const float both = fmaxf(__bfloat162float(mine), __bfloat162float(half_max[hh ^ 1]));
-            const float mn = both > m + 8.f ? both : m;
-            // O so far holds what the old base gave; each thread has half of its
-            // columns.  This tile's scores say that the product before is done.
+            for (int e = 0; e < 64; e += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(v[c0 + e + 2 * k])), __uint_as_float(v[c0 + e + 2 * k + 1]));
+          };
+          mask(0);
+          maxima(0);
+          tmem_ld_wait();
+          mask(64);
+          maxima(64);
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool far = mt > m + 8.f;
+          if (__any_sync(0xffffffffu, far)) {  // a segment's first tile, and seldom after
+            const float mn = far ? mt : m;
+            // O so far holds what the old base gave.  This tile's scores say that
+            // the product before is done.
             if (done > 0) {
               const float al = m == -INFINITY ? 0.f : ex2(m - mn);
               l *= al;
 #pragma unroll 1
-              for (int c = 0; c < DH / 32; ++c) {
+              for (int c = 0; c < DH / 16; ++c) {
                 uint32_t o[16];
-                tmem_ld_32x32b_x16(tO + hh * (DH / 2) + c * 16, o);
+                tmem_ld_32x32b_x16(tO + c * 16, o);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                tmem_st_32x32b_x16(tO + hh * (DH / 2) + c * 16, o);
+                tmem_st_32x32b_x16(tO + c * 16, o);
               }
             }
             m = mn;
           }
-          l += sum;
-          tmem_st_32x32b_x16(tS + hh * 32, p);
-          tmem_st_32x32b_x16(tS + hh * 32 + 16, p + 16);
+          const float base = m == -INFINITY ? 0.f : m;
+          float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float u = __uint_as_float(v[32 * h + 2 * e]), w = __uint_as_float(v[32 * h + 2 * e + 1]);
+              add2(u, w, -base, -base);
+              u = ex2(u);
+              w = ex2(w);
+              add2(sa[e & 1], sb[e & 1], u, w);
+              p[e] = pack2_bf16(u, w);
+            }
+            tmem_st_32x32b_x16(tS + h * 16, p);
+          }
+          l += (sa[0] + sb[0]) + (sa[1] + sb[1]);
           tmem_st_wait();
           // value rows past the sequence hold whatever the page does: zeros
           // (lane 0's P is waited for before either lane's product)
@@ -543,11 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             paged_wait(&full[n % G::kSlots], (uint32_t)(n / G::kSlots) & 1u, abort_flag);
             if (key_base + j * KT + r >= nkeys) {
 #pragma unroll
-              for (int c = 0; c < G::kHalves * 4; ++c) {
-                const int ch = hh * G::kHalves * 4 + c;
-                *reinterpret_cast<uint4*>(smem + G::kRingOff + (n % G::kSlots) * G::kTile + (ch >> 3) * G::kHalf +
-                                          r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
-              }
+              for (int c = 0; c < G::kHalves * 8; ++c)
+                *reinterpret_cast<uint4*>(smem + G::kRingOff + (n % G::kSlots) * G::kTile + (c >> 3) * G::kHalf +
+                                          r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_smem_async();
           }
@@ -556,43 +541,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&p_full[i]);
           ++cnt;
         }
-        // the row's sum from both halves
-        float* sums = reinterpret_cast<float*>(slot);
-        sums[hh] = l;
-        bar_pair(i, q);
-        l += sums[hh ^ 1];
-        bar_pair(i, q);  // both have read: the words are free again
         if (done > 0) {
           paged_wait(&pv_done[i], nend & 1u, abort_flag);
           ++nend;
           __syncwarp();
           tc_fence_after();
         }
-        // Two query tiles: a thread ends with half of its row's columns.  One:
-        // the lanes' results are joined, and it has a quarter (all four threads
-        // read the same tensor-memory lane).
-        int c0 = hh * (DH / 2), c1 = c0 + DH / 2;
+        // Two query tiles: a thread ends with its row.  One: the lanes' results
+        // are joined, and it has half of the columns (both threads read the
+        // same tensor-memory lane).
+        int c0 = 0, c1 = DH;
         float wa = 1.f, wb = 0.f;
         uint32_t ta = tO;
         const uint32_t tB = trow + 256 + 128;
         const bool two = !wide && nt > 1;
         if (!wide) {
-          if (hh == 0) {
-            sums[0] = l;
-            sums[1] = m;
-          }
+          row_ml[i * 128 + r] = make_float2(m, l);
           tc_fence_before();
           bar_all();
           tc_fence_after();
-          const float2 e0 = *reinterpret_cast<const float2*>(smem + G::kRowOff + r * 8);
-          const float2 e1 = *reinterpret_cast<const float2*>(smem + G::kRowOff + (128 + r) * 8);
-          m = fmaxf(e0.y, e1.y);
-          wa = e0.y == -INFINITY ? 0.f : ex2(e0.y - m);
-          wb = e1.y == -INFINITY ? 0.f : ex2(e1.y - m);
-          l = wa * e0.x + wb * e1.x;
+          const float2 e0 = row_ml[r], e1 = row_ml[128 + r];
+          m = fmaxf(e0.x, e1.x);
+          wa = e0.x == -INFINITY ? 0.f : ex2(e0.x - m);
+          wb = e1.x == -INFINITY ? 0.f : ex2(e1.x - m);
+          l = wa * e0.y + wb * e1.y;
           ta = trow + 256;
-          c0 = (i * 2 + hh) * (DH / 4);
-          c1 = c0 + DH / 4;
+          c0 = i * (DH / 2);
+          c1 = c0 + DH / 2;
         }
         auto columns = [&](int c, float* o) {  // columns c .. c+15 of the row
           tmem_ld_32x32b_x16(ta + c, reinterpret_cast<uint32_t*>(o));
@@ -645,9 +620,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           tc_fence_before();
-          if (hh == 0 && pi == i) *reinterpret_cast<float2*>(mine + 128 * DH + 2 * r) = make_float2(m, l);
+          if (pi == i) *reinterpret_cast<float2*>(mine + 128 * DH + 2 * r) = make_float2(m, l);
           if (wide) bar_lane(i); else bar_all();
-          if (r == 0 && hh == 0 && pi == i) {
+          if (r == 0 && pi == i) {
             const int before = arrive_acq_rel(a.counters + first * 2 + i);
             s_flag[i] = before == last - first;
             if (before == last - first) a.counters[first * 2 + i] = 0;  // ready for the next call
