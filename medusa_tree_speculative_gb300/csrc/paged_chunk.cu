@@ -30,6 +30,8 @@
 // MMAs that one thread issues run in issue order on the CTA's tensor core:
 // QK(j+1) may overwrite the columns from which PV(j), issued before it, reads
 // P.
+#include <utility>
+
 #include "paged_attn.cuh"
 #include "sm100.cuh"
 
@@ -39,7 +41,7 @@ namespace {
 using namespace sm100;
 
 constexpr int RB = 256, KT = 128;
-constexpr int kCost = 3;  // 8192 tokens: 535, 502, 486, 489 us at 1, 2, 3, 4
+constexpr int kCost = 2;  // 8192 tokens: 435, 438, 442 us at 2, 3, 4
 constexpr int kThreads = 384;  // two softmax groups of 128; the load warp, the MMA warp and two segment warps
 constexpr int kSoft = 256, kLoadWarp = 8, kMmaWarp = 9;
 // Registers: the block starts with 168 a thread (384 x 168 = 64512); the softmax
@@ -48,23 +50,29 @@ constexpr int kSoft = 256, kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kLaunchRegs = 168, kSoftRegs = 208, kOtherRegs = 88;
 static_assert(kSoft * kSoftRegs + (kThreads - kSoft) * kOtherRegs <= kThreads * kLaunchRegs, "registers");
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSmemBase = 1024;  // where dynamic shared memory starts in a kernel without static; checked
+
+template <uint32_t B>
+struct Half {
+  static constexpr uint32_t value = B;
+};
 
 template <int DH>
 struct Cfg {
   static constexpr int kHalves = DH / 64;
   static constexpr uint32_t kHalf = 128 * 128;          // 128 rows of one swizzle span
   static constexpr uint32_t kTile = kHalf * kHalves;    // 128 rows x DH bf16
-  static constexpr int kSlots = 4;  // K, V of an even tile, K, V of an odd one: their addresses are constants
+  static constexpr int kStages = 2;  // each the values of a tile and the keys of the next: one wait for both
   static constexpr uint32_t kRingOff = 2 * kTile;
-  static constexpr uint32_t kBarOff = kRingOff + kSlots * kTile;
-  static constexpr int kBars = 2 * kSlots + 2 + 2 + 2 + 1 + 1 + 1;
+  static constexpr uint32_t kBarOff = kRingOff + kStages * 2 * kTile;
+  static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 1 + 1 + 1;
   static constexpr uint32_t kSegOff = (kBarOff + kBars * 8 + 16 + 15) & ~15u;    // [2 lanes][2] segments
   static constexpr uint32_t kPlanOff = (kSegOff + 4 * sizeof(Segment) + 15) & ~15u;
   static constexpr uint32_t kRowOff = (kPlanOff + sizeof(Plan) + 15) & ~15u;  // [2 lanes][128 rows] 8 bytes
   static constexpr size_t smem = kRowOff + 2 * 128 * 8;
   static_assert(smem <= 232448, "shared memory");
   static constexpr int part_floats = 128 * DH + 2 * 128;  // one lane's partial
-  static_assert(sizeof(PlanScratch) <= kSlots * kTile, "the plan's scratch lies in the ring");
+  static_assert(sizeof(PlanScratch) <= kStages * 2 * kTile, "the plan's scratch lies in the ring");
 };
 
 // One thread of a converged warp, the same one every time.  The MMA's operands
@@ -108,24 +116,63 @@ MDEV void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-// MMAs from descriptor words (both descriptors' high words are the same), tensor
-// memory from column 0: a block that allocates all 512 columns gets them there.
-MDEV void umma_words(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc, uint32_t add) {
+// MMAs whose operands are all constants.  An MMA takes its descriptors and
+// addresses from warp-wide registers; anything that comes from a thread's
+// register is moved there first, six moves an MMA, which the issuing warp had
+// no time for beside the softmax.  Tensor memory starts at column 0: a block
+// that allocates all 512 columns gets them there.
+template <uint32_t D, uint64_t A, uint64_t B, uint32_t IDESC, bool ADD>
+MDEV void umma_const() {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 A, B;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\tmov.b64 A, {%1, %3};\n\tmov.b64 B, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], A, B, %4, p;\n\t}\n" ::"r"(d),
-      "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 A, B;\n\t.reg .b32 D, I;\n\t"
+      "mov.b32 D, %0;\n\tmov.b64 A, %1;\n\tmov.b64 B, %2;\n\tmov.b32 I, %3;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [D], A, B, I, p;\n\t}\n" ::"n"(D),
+      "n"(A), "n"(B), "n"(IDESC), "n"((int)ADD)
       : "memory");
 }
-MDEV void umma_ts_words(uint32_t d, uint32_t a, uint32_t blo, uint32_t hi, uint32_t idesc, uint32_t add) {
+template <uint32_t D, uint32_t A, uint64_t B, uint32_t IDESC>
+MDEV void umma_ts_const(uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 B;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\tmov.b64 B, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], B, %4, p;\n\t}\n" ::"r"(d),
-      "r"(a), "r"(blo), "r"(hi), "r"(idesc), "r"(add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 B;\n\t.reg .b32 A, D, I;\n\t"
+      "mov.b32 D, %0;\n\tmov.b32 A, %1;\n\tmov.b64 B, %2;\n\tmov.b32 I, %3;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [D], [A], B, I, p;\n\t}\n" ::"n"(D),
+      "n"(A), "n"(B), "n"(IDESC), "r"(add)
       : "memory");
 }
+// The products of lane I with the keys or values in stage B (QT: the query
+// tile).  Matrix descriptors: 128-byte swizzle, 1024 bytes between 8-row
+// groups; low word address / 16 and, for V, the bytes / 16 between its halves.
+template <int DH>
+struct Products {
+  using G = Cfg<DH>;
+  static constexpr uint64_t kHi = (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32;
+  static constexpr uint32_t kHalf16 = G::kHalf >> 4, kTile16 = G::kTile >> 4;
+  static constexpr uint32_t kQ = kSmemBase >> 4 | 1u << 16, kK = (kSmemBase + G::kRingOff) >> 4 | 1u << 16;
+  static constexpr uint32_t kV = ((kSmemBase + G::kRingOff) >> 4) + kTile16 | kHalf16 << 16;
+  static __host__ __device__ constexpr uint32_t step(int kk) { return (kk >> 2) * kHalf16 + (kk & 3) * 2; }
+  template <uint32_t I, uint32_t QT, uint32_t B, int... KK>
+  static MDEV void qk_steps(std::integer_sequence<int, KK...>) {
+    (umma_const<I * 128, kHi | (kQ + QT * kTile16 + step(KK)), kHi | (kK + B * 2 * kTile16 + step(KK)),
+                idesc_bf16_f32(128, KT), KK != 0>(),
+     ...);
+  }
+  template <uint32_t I, uint32_t B, int... J>
+  static MDEV void pv_steps(uint32_t add, std::integer_sequence<int, J...>) {
+    // V as stored, keys x values, is MN-major
+    (umma_ts_const<256 + I * 128, I * 128 + J * 8, kHi | (kV + B * 2 * kTile16 + J * (2048 >> 4)),
+                   idesc_bf16_f32(128, DH) | 1u << 16>(J == 0 ? add : 1u),
+     ...);
+  }
+  template <uint32_t I, uint32_t QT, uint32_t B>
+  static MDEV void qk() {
+    qk_steps<I, QT, B>(std::make_integer_sequence<int, DH / 16>());
+  }
+  template <uint32_t I, uint32_t B>
+  static MDEV void pv(uint32_t add) {
+    pv_steps<I, B>(add, std::make_integer_sequence<int, KT / 16>());
+  }
+};
+
 MDEV void commit_at(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
@@ -157,13 +204,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   using G = Cfg<DH>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  if (sbase & 1023) {  // the swizzle's atoms: there is no room to round the address up
+  if (sbase != kSmemBase) {
     if (threadIdx.x == 0) set_err(a.err, MEDUSA_DEVERR_TIMEOUT);
     return;
   }
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kBarOff);  // [slots] TMA -> MMA
-  uint64_t* empty = full + G::kSlots;                               // [slots] MMA -> TMA
-  uint64_t* s_full = empty + G::kSlots;                             // [2] MMA -> softmax: scores
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kBarOff);  // [stages] TMA -> MMA
+  uint64_t* empty = full + G::kStages;                              // [stages] MMA -> TMA
+  uint64_t* s_full = empty + G::kStages;                             // [2] MMA -> softmax: scores
   uint64_t* p_full = s_full + 2;                                    // [2] softmax -> MMA: P written, O rescaled
   uint64_t* pv_done = p_full + 2;                                   // [2] MMA -> softmax: the segment's O is complete
   uint64_t* q_full = pv_done + 2;
@@ -178,9 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < G::kSlots; ++i) {
+    for (int i = 0; i < G::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);  // its values are used, its keys are used
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -220,171 +267,161 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int op_run = lane / G::kHalves, op_half = lane % G::kHalves;
       const bool mine = op_run < runs;
       const int nowhere = (a.p.num_pages * a.Hkv) << a.p.shift;  // past the pool: reads zeros
-      int n = 0;
+      // stage n (n & 1): the values of the CTA's tile n - 1, the keys of tile n
+      int n = 0, yv = 0;
+      bool more = true;
+      int t = sg.t0;
       while (true) {
-        const SeqInfo& s = sg.s;
-        const int nkeys = s.L + s.n;
-        for (int t = sg.t0; t < sg.t1; ++t) {
+        int y = nowhere;
+        if (more) {
+          const SeqInfo& s = sg.s;
           const int key = t * KT + op_run * box;
-          int y = nowhere;
-          if (mine && key < nkeys) {
+          if (mine && key < s.L + s.n) {
             const int page = a.p.table[(int64_t)s.row * a.p.max_pages + (key >> a.p.shift)];
             if (page_ok(a.p, page)) y = (int)page_line(a.p, page, a.Hkv, sg.head, key & (a.p.page_size - 1));
             else set_err(a.err, MEDUSA_DEVERR_PAGE);
           }
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++n) {
-            const int sl = n % G::kSlots;
-            paged_wait(&empty[sl], ((uint32_t)(n / G::kSlots) & 1u) ^ 1u, abort_flag);
-            if (lane == 0) mbar_expect_tx(&full[sl], G::kTile);
-            __syncwarp();
-            if (mine)
-              tma_load_2d(smem + G::kRingOff + sl * G::kTile + op_half * G::kHalf + op_run * box * 128,
-                          kv ? &tmV : &tmK, &full[sl], op_half * 64, y);
-          }
         }
-        if (!next_segment<RB, KT, kCost>(a, pl, x1, sg)) break;
+        const int st = n & 1;
+        paged_wait(&empty[st], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag);
+        if (lane == 0) mbar_expect_tx(&full[st], (more ? G::kTile : 0u) + (n > 0 ? G::kTile : 0u));
+        __syncwarp();
+        uint8_t* dst = smem + G::kRingOff + st * 2 * G::kTile + op_half * G::kHalf + op_run * box * 128;
+        if (mine && n > 0) tma_load_2d(dst + G::kTile, &tmV, &full[st], op_half * 64, yv);
+        if (mine && more) tma_load_2d(dst, &tmK, &full[st], op_half * 64, y);
+        yv = y;
+        ++n;
+        if (!more) break;
+        if (++t == sg.t1) {
+          more = next_segment<RB, KT, kCost>(a, pl, x1, sg);
+          t = sg.t0;
+        }
       }
       // the copies in flight land before the CTA can end, whatever happened
-      for (int j = max(0, n - G::kSlots); j < n; ++j)
-        if (!mbar_wait(&full[j % G::kSlots], (uint32_t)(j / G::kSlots) & 1u)) *abort_flag = 1;
+      for (int j = max(0, n - 2); j < n; ++j)
+        if (!mbar_wait(&full[j & 1], (uint32_t)(j >> 1) & 1u)) *abort_flag = 1;
     } else if (warp == kMmaWarp && any) {
       // ------------------------------------------------ MMAs
-      // One warp issues 32 products' instructions per tile of 2048 cycles and
-      // competes with the softmax warps for issue slots, so this loop is kept
-      // short: addresses are constants (two tiles' ring slots in turn), what the
-      // MMAs read is the same in every lane for the compiler to see
-      // (warp-wide registers), barriers are waited for ahead of need, and there
-      // are as few commits as will do: QK(j+1)'s also says that PV(j), issued
-      // before it, is done.
-      auto uni = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
-      constexpr uint32_t idS = idesc_bf16_f32(128, KT);
-      constexpr uint32_t idPV = idesc_bf16_f32(128, DH) | (1u << 16);  // V as stored, keys x values: MN-major
-      // matrix descriptors: 128-byte swizzle, 1024 bytes between 8-row groups;
-      // low word: address / 16 and, for V, the bytes / 16 between its halves
-      constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
-      constexpr uint32_t kTile16 = G::kTile >> 4, kHalf16 = G::kHalf >> 4;
-      const uint32_t q16 = (sbase >> 4) | 1u << 16, k16 = ((sbase + G::kRingOff) >> 4) | 1u << 16;
-      const uint32_t v16 = ((sbase + G::kRingOff) >> 4) + kTile16 | kHalf16 << 16;
-      const uint32_t bars = smem_u32(full);
-      constexpr uint32_t kEmpty = 4 * 8, kS = 8 * 8, kP = 10 * 8, kPV = 12 * 8, kQ = 14 * 8, kQE = 15 * 8;
-      auto qk = [&](uint32_t d, uint32_t qa, uint32_t ka) {
-#pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk)
-          umma_words(d, qa + (kk >> 2) * kHalf16 + (kk & 3) * 2, ka + (kk >> 2) * kHalf16 + (kk & 3) * 2, kDescHi, idS,
-                     kk != 0);
-      };
-      auto pv = [&](uint32_t d, uint32_t va, uint32_t add) {
-#pragma unroll
-        for (int j = 0; j < KT / 16; ++j)
-          umma_ts_words(256 + d, d + j * 8, va + j * (2048 >> 4), kDescHi, idPV, j == 0 ? add : 1u);
-      };
-      uint32_t t = 0, ph0 = 0, ph1 = 0, qph = 0;  // the CTA's tiles so far; phases of p_full and q_full
-      uint32_t nt = 0, wide = 0;
-      auto enter = [&]() {
-        nt = uni(sg.t1 - sg.t0);
-        wide = uni(min(tb, sg.s.n - sg.u * tb) * a.g > 128);
-      };
-      enter();
-      bool ready = false;  // the segment's first scores are on their way
-      while (true) {
-        const uint32_t n = nt, w = wide;
-        const uint32_t more = uni(next_segment<RB, KT, kCost>(a, pl, x1, sg));
-        if (more) enter();
-        const bool chain = more && w && wide;  // the next segment's first scores follow this one's last
-        if (!ready) {
-          wait_at(bars + kQ, qph, abort_flag);
-          qph ^= 1u;
-          for (uint32_t i = 0; i < 2 && (w ? i < 1 : i < n); ++i) {
-            const uint32_t b = uni((t + i) & 1u);
-            wait_at(bars + b * 16, (t + i) >> 1 & 1u, abort_flag);
-            tc_fence_after();
-            if (elect_one()) {
-              qk(i * 128, q16, k16 + b * 2 * kTile16);
-              commit_at(bars + kS + i * 8);
+      // One thread issues 32 products' instructions per tile of 2048 cycles.
+      // Issuing does not run ahead of the tensor core by more than an
+      // instruction or two, and beside the softmax warps a wait costs 150
+      // cycles even where it is over: so addresses are constants, and there are
+      // as few waits and commits as will do (QK(j+1)'s commit also says that
+      // PV(j), issued before it, is done).
+      if (elect_one()) {
+        using P = Products<DH>;
+        constexpr uint32_t bars = kSmemBase + G::kBarOff;
+        constexpr uint32_t kEmpty = bars + 2 * 8, kS = bars + 4 * 8, kP = bars + 6 * 8, kPV = bars + 8 * 8,
+                           kQ = bars + 10 * 8, kQE = bars + 11 * 8, kDone = bars + 12 * 8;
+        uint32_t t = 0, ph0 = 0, ph1 = 0, qph = 0;  // the CTA's tiles so far; phases of p_full and q_full
+        uint32_t nt = sg.t1 - sg.t0, wide = min(tb, sg.s.n - sg.u * tb) * a.g > 128;
+        bool ready = false;  // the segment's first scores are on their way
+        while (true) {
+          const uint32_t n = nt, w = wide;
+          const bool more = next_segment<RB, KT, kCost>(a, pl, x1, sg);
+          if (more) {
+            nt = sg.t1 - sg.t0;
+            wide = min(tb, sg.s.n - sg.u * tb) * a.g > 128;
+          }
+          const bool chain = more && w && wide;  // the next segment's first scores follow this one's last
+          // QK of lane 0 (or, narrow, of lane i) with the keys of tile u
+          auto one = [&](uint32_t i, uint32_t u) {
+            if (i == 0) {
+              if (u & 1u) P::template qk<0, 0, 1>(); else P::template qk<0, 0, 0>();
+            } else {
+              if (u & 1u) P::template qk<1, 0, 1>(); else P::template qk<1, 0, 0>();
+            }
+            commit_at(kS + i * 8);
+          };
+          if (!ready) {
+            wait_at(kQ, qph, abort_flag);
+            qph ^= 1u;
+            for (uint32_t i = 0; i < 2 && (w ? i < 1 : i < n); ++i) {
+              const uint32_t u = t + i;
+              wait_at(bars + (u & 1u) * 8, u >> 1 & 1u, abort_flag);
+              tc_fence_after();
+              one(i, u);
               if (w) {
-                qk(128, q16 + kTile16, k16 + b * 2 * kTile16);
-                commit_at(bars + kS + 8);
+                if (u & 1u) P::template qk<1, 1, 1>(); else P::template qk<1, 1, 0>();
+                commit_at(kS + 8);
               }
-              commit_at(bars + kEmpty + b * 16);
-              if (w ? n == 1 : i + 1 == n) commit_at(bars + kQE);
+              commit_at(kEmpty + (u & 1u) * 8);
+              if (u == 0) commit_at(kEmpty);  // the first stage has no values
+              if (w ? n == 1 : i + 1 == n) commit_at(kQE);
             }
-            __syncwarp();
           }
-        }
-        if (w) {
-          // PV0(j), QK0(j + 1), PV1(j), QK1(j + 1): one copy of the code for both
-          // lanes and ring halves (unrolled by them it was 5% slower: the
-          // instruction cache also holds the softmax)
-          for (uint32_t j = 0; j < n; ++j, ++t) {
-            const uint32_t b = uni(t & 1u), end = uni(j + 1 == n), go = uni(!end || chain);
-            const uint32_t qe = uni(j + 2 == n || (end && chain && nt == 1));
-            wait_at(bars + b * 16 + 8, t >> 1 & 1u, abort_flag);  // ahead of P
-#pragma unroll 1
-            for (uint32_t i = 0; i < 2; ++i) {
-              wait_at(bars + kP + i * 8, i ? ph1 : ph0, abort_flag);
+          if (w) {
+            // tile t with its keys in stage B and its values in the other one:
+            // PV0(t), QK0(t + 1), PV1(t), QK1(t + 1)
+            auto tile = [&](auto stage, uint32_t j) {
+              constexpr uint32_t B = decltype(stage)::value, O = B ^ 1;
+              const bool end = j + 1 == n, go = !end || chain;
+              wait_at(bars + O * 8, (t + 1) >> 1 & 1u, abort_flag);  // V(t) and K(t + 1)
+              wait_at(kP, ph0, abort_flag);
               tc_fence_after();
-              if (elect_one()) {
-                pv(i * 128, v16 + b * 2 * kTile16, j > 0);
-                if (i) commit_at(bars + kEmpty + b * 16 + 8);
-                if (end) commit_at(bars + kPV + i * 8);
-              }
-              __syncwarp();
+              P::template pv<0, O>(j > 0);
               if (go) {
-                if (i == 0) {
-                  if (end) {
-                    wait_at(bars + kQ, qph, abort_flag);
-                    qph ^= 1u;
-                  }
-                  wait_at(bars + (b ^ 1) * 16, (t + 1) >> 1 & 1u, abort_flag);
-                  tc_fence_after();
+                if (end) {
+                  commit_at(kPV);
+                  wait_at(kQ, qph, abort_flag);
+                  qph ^= 1u;
                 }
-                if (elect_one()) {
-                  qk(i * 128, q16 + i * kTile16, k16 + (b ^ 1) * 2 * kTile16);
-                  commit_at(bars + kS + i * 8);
-                  if (i) commit_at(bars + kEmpty + (b ^ 1) * 16);
-                  if (i && qe) commit_at(bars + kQE);
-                }
-                __syncwarp();
+                P::template qk<0, 0, O>();
+                commit_at(kS);
+              } else {
+                commit_at(kPV);
               }
-            }
-            ph0 ^= 1u;
-            ph1 ^= 1u;
-          }
-          ready = chain;
-        } else {
-          for (uint32_t j = 0; j < n; ++j) {
-            const uint32_t i = uni(j & 1u), b = uni(t & 1u);
-            wait_at(bars + b * 16 + 8, t >> 1 & 1u, abort_flag);
-            wait_at(bars + kP + i * 8, i ? ph1 : ph0, abort_flag);
-            if (i) ph1 ^= 1u; else ph0 ^= 1u;
-            tc_fence_after();
-            const bool go = j + 2 < n;
-            if (elect_one()) {
-              pv(i * 128, v16 + b * 2 * kTile16, j > 1);
-              commit_at(bars + kEmpty + b * 16 + 8);
-              if (!go) commit_at(bars + kPV + i * 8);
-            }
-            __syncwarp();
-            if (go) {
-              wait_at(bars + b * 16, (t + 2) >> 1 & 1u, abort_flag);
+              wait_at(kP + 8, ph1, abort_flag);
               tc_fence_after();
-              if (elect_one()) {
-                qk(i * 128, q16, k16 + b * 2 * kTile16);
-                commit_at(bars + kS + i * 8);
-                commit_at(bars + kEmpty + b * 16);
-                if (j + 3 == n) commit_at(bars + kQE);
+              P::template pv<1, O>(j > 0);
+              commit_at(kEmpty + O * 8);
+              if (end) commit_at(kPV + 8);
+              if (go) {
+                P::template qk<1, 1, O>();
+                commit_at(kS + 8);
+                commit_at(kEmpty + O * 8);
+                if (j + 2 == n || (end && nt == 1)) commit_at(kQE);
               }
-              __syncwarp();
+              ph0 ^= 1u;
+              ph1 ^= 1u;
+              ++t;
+            };
+            for (uint32_t j = 0; j < n; ++j) {
+              if (t & 1u) tile(Half<1>(), j);
+              else tile(Half<0>(), j);
             }
-            ++t;
+            ready = chain;
+          } else {
+            for (uint32_t j = 0; j < n; ++j) {
+              const uint32_t i = j & 1u, o = (t + 1) & 1u;
+              wait_at(bars + o * 8, (t + 1) >> 1 & 1u, abort_flag);
+              wait_at(kP + i * 8, i ? ph1 : ph0, abort_flag);
+              if (i) ph1 ^= 1u; else ph0 ^= 1u;
+              tc_fence_after();
+              if (i == 0) {
+                if (o) P::template pv<0, 1>(j > 1); else P::template pv<0, 0>(j > 1);
+              } else {
+                if (o) P::template pv<1, 1>(j > 1); else P::template pv<1, 0>(j > 1);
+              }
+              commit_at(kEmpty + o * 8);
+              if (j + 2 < n) {
+                wait_at(bars + (t & 1u) * 8, (t + 2) >> 1 & 1u, abort_flag);
+                tc_fence_after();
+                one(i, t + 2);
+                commit_at(kEmpty + (t & 1u) * 8);
+                if (j + 3 == n) commit_at(kQE);
+              } else {
+                commit_at(kPV + i * 8);
+              }
+              ++t;
+            }
+            ready = false;
           }
-          ready = false;
+          if (!more) break;
         }
-        if (!more) break;
+        commit_at(kDone);
+        wait_at(kDone, 0, abort_flag);
       }
-      if (elect_one()) umma_commit(all_done);
-      if (!mbar_wait(all_done, 0)) *abort_flag = 1;
       __syncwarp();
     } else if (warp > kMmaWarp && any) {
       // ------------------------------------------------ a lane's segments
@@ -526,12 +563,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           // value rows past the sequence hold whatever the page does: zeros
           // (lane 0's P is waited for before either lane's product)
           if (key_base + (j + 1) * KT > nkeys && (i == 0 || !wide)) {
-            const int n = 2 * (it + j) + 1;
-            paged_wait(&full[n % G::kSlots], (uint32_t)(n / G::kSlots) & 1u, abort_flag);
+            const int n = it + j + 1;  // the values' stage
+            paged_wait(&full[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
             if (key_base + j * KT + r >= nkeys) {
 #pragma unroll
               for (int c = 0; c < G::kHalves * 8; ++c)
-                *reinterpret_cast<uint4*>(smem + G::kRingOff + (n % G::kSlots) * G::kTile + (c >> 3) * G::kHalf +
+                *reinterpret_cast<uint4*>(smem + G::kRingOff + (n & 1) * 2 * G::kTile + G::kTile + (c >> 3) * G::kHalf +
                                           r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_smem_async();
