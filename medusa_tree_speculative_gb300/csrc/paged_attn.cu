@@ -2,6 +2,7 @@
 // chunk, and the float32 kernels.
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "paged_attn.cuh"
 
@@ -9,14 +10,16 @@ namespace medusa {
 namespace {
 
 // ------------------------------------------------ rotate, scale, append --
-// A CTA per kPrepTokens tokens and group of heads: cos and sin of a token's
-// position once per pair, in shared memory, then eight pairs per thread and
-// step.  Queries go to q_rot with the softmax scale in them, keys and values
-// to their pages.  Every element is read and written once: bound by memory for
-// long chunks, by the latency of a thread's few steps for short ones, so the
-// heads are cut into as many groups as give a thread two steps.
-constexpr int kPrepTokens = 4;
+// A CTA per TOK tokens and group of heads: cos and sin of a token's position
+// once per pair, in shared memory, then eight pairs per thread and step, the
+// loads of kPrepSteps steps in flight.  Queries go to q_rot with the softmax
+// scale in them, keys and values to their pages.  Every element is read and
+// written once: bound by memory for long chunks (16 tokens per CTA, all heads:
+// 8192 tokens of 48 heads in XXX us), by the latency of a thread's few steps
+// for short ones (4 tokens, as many groups of heads as give a thread
+// kPrepSteps).
 constexpr int kPrepThreads = 256;
+constexpr int kPrepSteps = 4;
 
 template <typename T>
 MDEV void load8(const T* p, float* f);
@@ -43,79 +46,123 @@ MDEV void store8<uint16_t>(uint16_t* p, const float* f) {
       make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
 }
 
-template <typename T, int DH>
+template <typename T, int DH, int TOK>
 __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_constant__ PagedAttnArgs a) {
-  __shared__ float cs[kPrepTokens][DH / 2], sn[kPrepTokens][DH / 2];
-  __shared__ int64_t line0[kPrepTokens];  // head 0's line of the token's slot, -1: no page
-  __shared__ int use[kPrepTokens], pos[kPrepTokens];
-  const int t = threadIdx.x, tok0 = blockIdx.x * kPrepTokens, nt = min(kPrepTokens, a.total_q - tok0);
-  for (int k = 0; k < nt; ++k) {
-    const int tok = tok0 + k;
-    int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before the token
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.q_start[mid] <= tok) lo = mid; else hi = mid - 1;
-    }
-    SeqInfo s;
-    int code;
-    bool ok = seq_info(a, lo, s, code) && tok >= s.q0 && tok < s.q0 + s.n;
-    bool twice = false;
-    if (ok && a.rows)  // an entry whose row an earlier one names is skipped
-      for (int j = t; j < lo; j += kPrepThreads) twice |= a.rows[j] == s.row && a.q_start[j + 1] > a.q_start[j];
-    twice = __syncthreads_or(twice);
-    if (t == 0) {
-      ok = ok && !twice;
-      use[k] = ok;
-      pos[k] = 0;
-      line0[k] = -1;
-      if (ok) {
+  __shared__ __align__(16) float cs[TOK][DH / 2], sn[TOK][DH / 2];
+  __shared__ int64_t line0[TOK];  // head 0's line of the token's slot, -1: no page
+  __shared__ int use[TOK], pos[TOK], seq[TOK], twice[TOK];
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // they wait for this grid's end
+  const int t = threadIdx.x, tok0 = blockIdx.x * TOK, nt = min(TOK, a.total_q - tok0);
+  if (t < TOK) {
+    seq[t] = -1;
+    use[t] = 0;
+    twice[t] = 0;
+    pos[t] = 0;
+    line0[t] = -1;
+    if (t < nt) {
+      const int tok = tok0 + t;
+      int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before the token
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.q_start[mid] <= tok) lo = mid; else hi = mid - 1;
+      }
+      SeqInfo s;
+      int code;
+      if (seq_info(a, lo, s, code) && tok >= s.q0 && tok < s.q0 + s.n) {
         const int i = tok - s.q0;
-        pos[k] = s.L + (a.T ? min(max(a.depth[i], 0), a.K) : i);
+        seq[t] = lo;
+        use[t] = 1;
+        pos[t] = s.L + (a.T ? min(max(a.depth[i], 0), a.K) : i);
         const int page = page_of(a, s, s.L + i);
-        if (page >= 0) line0[k] = page_line(a.p, page, a.Hkv, 0, (s.L + i) & (a.p.page_size - 1));
+        if (page >= 0) line0[t] = page_line(a.p, page, a.Hkv, 0, (s.L + i) & (a.p.page_size - 1));
       }
     }
   }
   __syncthreads();
+  if (a.rows) {  // an entry whose row an earlier one names is skipped
+    for (int k = 0; k < nt; ++k) {
+      const int b = seq[k];
+      if (b > 0 && (k == 0 || seq[k - 1] != b))
+        for (int j = t; j < b; j += kPrepThreads)
+          if (a.rows[j] == a.rows[b] && a.q_start[j + 1] > a.q_start[j]) twice[k] = 1;
+    }
+  }
   for (int e = t; e < nt * (DH / 2); e += kPrepThreads)
     rope_cos_sin(pos[e / (DH / 2)], a.turns[e % (DH / 2)], cs[e / (DH / 2)][e % (DH / 2)],
                  sn[e / (DH / 2)][e % (DH / 2)]);
   __syncthreads();
-  constexpr int kChunks = DH / 16;  // runs of eight pairs in a head
-  const int all = a.H + 2 * a.Hkv, per = (all + gridDim.y - 1) / gridDim.y;
-  const int head0 = blockIdx.y * per, heads = min(per, all - head0), items = nt * heads * kChunks;
-  const T* q = static_cast<const T*>(a.q);
-  for (int e = t; e < items; e += kPrepThreads) {
-    const int c = e % kChunks, h = head0 + e / kChunks % heads, k = e / (kChunks * heads);
-    if (!use[k]) continue;
-    const int64_t tok = tok0 + k;
-    float lo[8], hi[8];
-    const T* src = h < a.H ? q + tok * a.q_stride + (int64_t)h * DH
-                   : h < a.H + a.Hkv ? static_cast<const T*>(a.k_new) + tok * a.k_stride + (int64_t)(h - a.H) * DH
-                                     : static_cast<const T*>(a.v_new) + tok * a.v_stride +
-                                           (int64_t)(h - a.H - a.Hkv) * DH;
-    T* dst;
-    if (h < a.H) {
-      dst = static_cast<T*>(a.q_rot) + (((int64_t)(h / a.g) * a.total_q + tok) * a.g + h % a.g) * DH;
-    } else {
-      if (line0[k] < 0) continue;
-      const int hk = h < a.H + a.Hkv ? h - a.H : h - a.H - a.Hkv;
-      dst = static_cast<T*>(h < a.H + a.Hkv ? a.k_pages : a.v_pages) +
-            (line0[k] + ((int64_t)hk << a.p.shift)) * DH;
+  if (a.rows && t == 0)
+    for (int k = 0; k < nt; ++k) {
+      if (k > 0 && seq[k - 1] == seq[k]) twice[k] = twice[k - 1];
+      if (twice[k]) use[k] = 0;
     }
-    load8(src + c * 8, lo);
-    load8(src + DH / 2 + c * 8, hi);
-    if (h < a.H + a.Hkv) {
-      const float mul = h < a.H ? a.qscale : 1.f;
+  if (a.rows) __syncthreads();
+  constexpr int kChunks = DH / 16;  // runs of eight pairs in a head
+  constexpr int kRows = kPrepThreads / kChunks;
+  const int all = a.H + 2 * a.Hkv, per = (all + gridDim.y - 1) / gridDim.y;
+  const int head0 = blockIdx.y * per, heads = min(per, all - head0), rows = nt * heads;
+  const int c = t % kChunks;
+  const float inv = 1.f / (float)heads;
+  using V = uint4;
+  constexpr int kVecs = 8 * sizeof(T) / 16;  // 16-byte loads of eight elements
+  for (int r0 = t / kChunks; r0 < rows; r0 += kPrepSteps * kRows) {
+    V lo[kPrepSteps][kVecs], hi[kPrepSteps][kVecs];
+    T* dst[kPrepSteps];
+    int tk[kPrepSteps];  // token, or -1 - token where nothing turns; kNone: nothing to do
+    constexpr int kNone = 1 << 20;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float co = cs[k][c * 8 + j], si = sn[k][c * 8 + j], x = lo[j], y = hi[j];
-        lo[j] = (x * co - y * si) * mul;
-        hi[j] = (y * co + x * si) * mul;
+    for (int u = 0; u < kPrepSteps; ++u) {
+      const int r = r0 + u * kRows;
+      tk[u] = kNone;
+      if (r >= rows) continue;
+      const int k = (int)(((float)r + 0.5f) * inv), h = head0 + r - k * heads;  // exact: rows and heads are small
+      if (!use[k]) continue;
+      const int64_t tok = tok0 + k;
+      const T* src;
+      if (h < a.H) {
+        src = static_cast<const T*>(a.q) + tok * a.q_stride + (int64_t)h * DH;
+        const int hk = h / a.g;
+        dst[u] = static_cast<T*>(a.q_rot) + (((int64_t)hk * a.total_q + tok) * a.g + h - hk * a.g) * DH;
+        tk[u] = k;
+      } else {
+        if (line0[k] < 0) continue;
+        const bool key = h < a.H + a.Hkv;
+        const int hk = key ? h - a.H : h - a.H - a.Hkv;
+        src = key ? static_cast<const T*>(a.k_new) + tok * a.k_stride + (int64_t)hk * DH
+                  : static_cast<const T*>(a.v_new) + tok * a.v_stride + (int64_t)hk * DH;
+        dst[u] = static_cast<T*>(key ? a.k_pages : a.v_pages) + (line0[k] + ((int64_t)hk << a.p.shift)) * DH;
+        tk[u] = key ? k : -1 - k;
+      }
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        lo[u][v] = __ldg(reinterpret_cast<const V*>(src + c * 8) + v);
+        hi[u][v] = __ldg(reinterpret_cast<const V*>(src + DH / 2 + c * 8) + v);
       }
     }
-    store8(dst + c * 8, lo);
-    store8(dst + DH / 2 + c * 8, hi);
+#pragma unroll
+    for (int u = 0; u < kPrepSteps; ++u) {
+      if (tk[u] == kNone) continue;
+      if (tk[u] >= 0) {
+        const int h = head0 + (r0 + u * kRows) - tk[u] * heads;
+        const float mul = h < a.H ? a.qscale : 1.f;
+        float x[8], y[8];
+        load8(reinterpret_cast<const T*>(lo[u]), x);
+        load8(reinterpret_cast<const T*>(hi[u]), y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float co = cs[tk[u]][c * 8 + j], si = sn[tk[u]][c * 8 + j], p = x[j], q = y[j];
+          x[j] = (p * co - q * si) * mul;
+          y[j] = (q * co + p * si) * mul;
+        }
+        store8(reinterpret_cast<T*>(lo[u]), x);
+        store8(reinterpret_cast<T*>(hi[u]), y);
+      }
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        *(reinterpret_cast<V*>(dst[u] + c * 8) + v) = lo[u][v];
+        *(reinterpret_cast<V*>(dst[u] + DH / 2 + c * 8) + v) = hi[u][v];
+      }
+    }
   }
 }
 
@@ -126,13 +173,15 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_c
 // its maximum and sum are four shuffles.  Key rows are padded by 16 bytes
 // (eight threads' 16-byte loads of eight rows then hit different banks).  The
 // value tile loads while S is computed and the next key tile while O is.
-constexpr int kGenThreads = 256;
+constexpr int kGenThreads = 256, kGenCtas = 2;  // CTAs per SM
 
 template <int DH, int RB, int KT>
 struct Gen {
   static constexpr int TM = RB / 16, TN = KT / 16, CC = DH / 64;
   static constexpr int kQ = RB * (DH + 4), kK = KT * (DH + 4), kV = KT * DH, kP = RB * (KT + 4);
-  static constexpr size_t smem = (size_t)(kQ + kK + kV + kP) * 4 + sizeof(PlanScratch) + sizeof(Plan) + 64;
+  // the plan's scratch lies where the tiles come later
+  static constexpr size_t smem = (size_t)(kQ + kK + kV + kP) * 4 + sizeof(Plan) + 64;
+  static_assert(sizeof(PlanScratch) <= (size_t)(kQ + kK) * 4, "the plan's scratch");
   static constexpr int part_floats = RB * DH + 2 * RB;
 };
 
@@ -144,8 +193,8 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
   float* Ks = Qs + G::kQ;          // [KT][DH + 4]
   float* Vs = Ks + G::kK;          // [KT][DH]
   float* Ps = Vs + G::kV;          // [RB][KT + 4]
-  PlanScratch& sc = *reinterpret_cast<PlanScratch*>(Ps + G::kP);
-  Plan& pl = *reinterpret_cast<Plan*>(&sc + 1);
+  PlanScratch& sc = *reinterpret_cast<PlanScratch*>(sm);
+  Plan& pl = *reinterpret_cast<Plan*>(Ps + G::kP);
   int* flag = reinterpret_cast<int*>(&pl + 1);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   int64_t x, x1;
@@ -154,6 +203,7 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
   const int tb = RB / a.g;
   Segment sg;
   if (x >= x1 || !seek_segment<RB, KT, 1>(a, sc, x, x1, sg)) return;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the rotated queries and the appended tokens
   while (true) {
     const SeqInfo& s = sg.s;
     const int nkeys = s.L + s.n, tok0 = sg.u * tb, live = min(tb, s.n - tok0) * a.g;
@@ -194,86 +244,93 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
 #pragma unroll
       for (int c = 0; c < G::CC * 4; ++c) o[i][c] = 0.f;
     }
-    for (int t = sg.t0; t < sg.t1; ++t) {
-      cp_async_wait<1>();  // this tile's keys
-      __syncthreads();
-      float z[G::TM][G::TN] = {};
+    // a block with at most 16 rows (a single token beside longer chunks) has
+    // them all in i = 0
+    auto tiles = [&](auto active) {
+      constexpr int N = decltype(active)::value;
+      for (int t = sg.t0; t < sg.t1; ++t) {
+        cp_async_wait<1>();  // this tile's keys
+        __syncthreads();
+        float z[N][G::TN] = {};
 #pragma unroll 4
-      for (int d = 0; d < DH; d += 4) {
-        float4 qv[G::TM], kv[G::TN];
+        for (int d = 0; d < DH; d += 4) {
+          float4 qv[N], kv[G::TN];
 #pragma unroll
-        for (int i = 0; i < G::TM; ++i) qv[i] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * (DH + 4) + d);
+          for (int i = 0; i < N; ++i) qv[i] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * (DH + 4) + d);
 #pragma unroll
-        for (int j = 0; j < G::TN; ++j) kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * (DH + 4) + d);
+          for (int j = 0; j < G::TN; ++j) kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * (DH + 4) + d);
 #pragma unroll
-        for (int i = 0; i < G::TM; ++i)
+          for (int i = 0; i < N; ++i)
 #pragma unroll
-          for (int j = 0; j < G::TN; ++j)
-            z[i][j] += qv[i].x * kv[j].x + qv[i].y * kv[j].y + qv[i].z * kv[j].z + qv[i].w * kv[j].w;
-      }
-      __syncthreads();  // the keys are read
-      if (t + 1 < sg.t1) load(a.k_pages, Ks, DH + 4, t + 1);
-      else cp_async_commit();
-      const bool masked = (t + 1) * KT > s.L;  // keys past the prefix: the mask decides
+            for (int j = 0; j < G::TN; ++j)
+              z[i][j] += qv[i].x * kv[j].x + qv[i].y * kv[j].y + qv[i].z * kv[j].z + qv[i].w * kv[j].w;
+        }
+        __syncthreads();  // the keys are read
+        if (t + 1 < sg.t1) load(a.k_pages, Ks, DH + 4, t + 1);
+        else cp_async_commit();
+        const bool masked = (t + 1) * KT > s.L;  // keys past the prefix: the mask decides
 #pragma unroll
-      for (int i = 0; i < G::TM; ++i) {
-        const int r = ty + 16 * i, tok = tok0 + r / a.g;
-        if (masked) {
+        for (int i = 0; i < N; ++i) {
+          const int r = ty + 16 * i, tok = tok0 + r / a.g;
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < G::TN; ++j) {
+              const int key = t * KT + tx + 16 * j;
+              if (r >= live || key >= nkeys || !key_seen(a, s, tok, key)) z[i][j] = -INFINITY;
+            }
+          }
+          float mt = z[i][0];
+#pragma unroll
+          for (int j = 1; j < G::TN; ++j) mt = fmaxf(mt, z[i][j]);
+#pragma unroll
+          for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, w));
+          const float mn = fmaxf(m[i], mt), base = mn == -INFINITY ? 0.f : mn;
+          const float alpha = exp2f(m[i] - base);
+          m[i] = mn;
+          float sum = 0.f;
 #pragma unroll
           for (int j = 0; j < G::TN; ++j) {
-            const int key = t * KT + tx + 16 * j;
-            if (r >= live || key >= nkeys || !key_seen(a, s, tok, key)) z[i][j] = -INFINITY;
+            const float pj = exp2f(z[i][j] - base);
+            sum += pj;
+            Ps[r * (KT + 4) + tx + 16 * j] = pj;
           }
+          l[i] = l[i] * alpha + sum;  // this thread's keys; the sixteen parts are added at the end
+#pragma unroll
+          for (int c = 0; c < G::CC * 4; ++c) o[i][c] *= alpha;
         }
-        float mt = z[i][0];
-#pragma unroll
-        for (int j = 1; j < G::TN; ++j) mt = fmaxf(mt, z[i][j]);
-#pragma unroll
-        for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, w));
-        const float mn = fmaxf(m[i], mt), base = mn == -INFINITY ? 0.f : mn;
-        const float alpha = exp2f(m[i] - base);
-        m[i] = mn;
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < G::TN; ++j) {
-          const float pj = exp2f(z[i][j] - base);
-          sum += pj;
-          Ps[r * (KT + 4) + tx + 16 * j] = pj;
-        }
-        l[i] = l[i] * alpha + sum;  // this thread's keys; the sixteen parts are added at the end
-#pragma unroll
-        for (int c = 0; c < G::CC * 4; ++c) o[i][c] *= alpha;
-      }
-      cp_async_wait<1>();  // this tile's values
-      __syncthreads();
+        cp_async_wait<1>();  // this tile's values
+        __syncthreads();
 #pragma unroll 2
-      for (int k = 0; k < KT; k += 4) {
-        float4 pv[G::TM];
+        for (int k = 0; k < KT; k += 4) {
+          float4 pv[N];
 #pragma unroll
-        for (int i = 0; i < G::TM; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * (KT + 4) + k);
+          for (int i = 0; i < N; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * (KT + 4) + k);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          float4 vv[G::CC];
+          for (int kk = 0; kk < 4; ++kk) {
+            float4 vv[G::CC];
 #pragma unroll
-          for (int c = 0; c < G::CC; ++c)
-            vv[c] = *reinterpret_cast<const float4*>(Vs + (k + kk) * DH + tx * 4 + 64 * c);
+            for (int c = 0; c < G::CC; ++c)
+              vv[c] = *reinterpret_cast<const float4*>(Vs + (k + kk) * DH + tx * 4 + 64 * c);
 #pragma unroll
-          for (int i = 0; i < G::TM; ++i) {
-            const float pj = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
+            for (int i = 0; i < N; ++i) {
+              const float pj = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
 #pragma unroll
-            for (int c = 0; c < G::CC; ++c) {
-              o[i][c * 4] += pj * vv[c].x;
-              o[i][c * 4 + 1] += pj * vv[c].y;
-              o[i][c * 4 + 2] += pj * vv[c].z;
-              o[i][c * 4 + 3] += pj * vv[c].w;
+              for (int c = 0; c < G::CC; ++c) {
+                o[i][c * 4] += pj * vv[c].x;
+                o[i][c * 4 + 1] += pj * vv[c].y;
+                o[i][c * 4 + 2] += pj * vv[c].z;
+                o[i][c * 4 + 3] += pj * vv[c].w;
+              }
             }
           }
         }
+        __syncthreads();  // the values are read
+        if (t + 1 < sg.t1) load(a.v_pages, Vs, DH, t + 1);
+        else cp_async_commit();
       }
-      __syncthreads();  // the values are read
-      if (t + 1 < sg.t1) load(a.v_pages, Vs, DH, t + 1);
-      else cp_async_commit();
-    }
+    };
+    if (live <= 16) tiles(std::integral_constant<int, 1>());
+    else tiles(std::integral_constant<int, G::TM>());
 #pragma unroll
     for (int i = 0; i < G::TM; ++i)
 #pragma unroll
@@ -312,30 +369,43 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
         if (before == last - first) a.counters[first] = 0;  // ready for the next call
       }
       __syncthreads();
-      if (*flag) {
+      if (*flag) {  // one partial at a time, all its rows' loads in flight
 #pragma unroll
         for (int i = 0; i < G::TM; ++i) {
-          const int r = ty + 16 * i;
-          float M = -INFINITY, sum = 0.f, acc[G::CC * 4] = {};
-          for (int c = first; c <= last; ++c)
-            M = fmaxf(M, __ldcg(a.part + (int64_t)part_slot(sg.unit_x, c, total, grid) * G::part_floats + RB * DH +
-                                2 * r));
-          for (int c = first; c <= last; ++c) {
-            const float* pt = a.part + (int64_t)part_slot(sg.unit_x, c, total, grid) * G::part_floats;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pt + RB * DH + 2 * r));
-            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-            sum += w * ml.y;
+          m[i] = -INFINITY;
+          l[i] = 0.f;
+#pragma unroll
+          for (int c = 0; c < G::CC * 4; ++c) o[i][c] = 0.f;
+        }
+        for (int c = first; c <= last; ++c) {
+          const float* pt = a.part + (int64_t)part_slot(sg.unit_x, c, total, grid) * G::part_floats;
+          float2 ml[G::TM];
+          float4 v[G::TM][G::CC];
+#pragma unroll
+          for (int i = 0; i < G::TM; ++i) {
+            const int r = ty + 16 * i;
+            ml[i] = __ldcg(reinterpret_cast<const float2*>(pt + RB * DH + 2 * r));
+#pragma unroll
+            for (int cc = 0; cc < G::CC; ++cc)
+              v[i][cc] = __ldcg(reinterpret_cast<const float4*>(pt + r * DH + tx * 4 + 64 * cc));
+          }
+#pragma unroll
+          for (int i = 0; i < G::TM; ++i) {
+            const float N = fmaxf(m[i], ml[i].x);
+            const float f0 = m[i] == -INFINITY ? 0.f : exp2f(m[i] - N), f1 = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - N);
+            m[i] = N;
+            l[i] = l[i] * f0 + ml[i].y * f1;
 #pragma unroll
             for (int cc = 0; cc < G::CC; ++cc) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(pt + r * DH + tx * 4 + 64 * cc));
-              acc[cc * 4] += w * v.x;
-              acc[cc * 4 + 1] += w * v.y;
-              acc[cc * 4 + 2] += w * v.z;
-              acc[cc * 4 + 3] += w * v.w;
+              o[i][cc * 4] = o[i][cc * 4] * f0 + v[i][cc].x * f1;
+              o[i][cc * 4 + 1] = o[i][cc * 4 + 1] * f0 + v[i][cc].y * f1;
+              o[i][cc * 4 + 2] = o[i][cc * 4 + 2] * f0 + v[i][cc].z * f1;
+              o[i][cc * 4 + 3] = o[i][cc * 4 + 3] * f0 + v[i][cc].w * f1;
             }
           }
-          put(i, acc, sum);
         }
+#pragma unroll
+        for (int i = 0; i < G::TM; ++i) put(i, o[i], l[i]);
       }
     }
     if (!next_segment<RB, KT, 1>(a, pl, x1, sg)) break;
@@ -348,11 +418,11 @@ int run_generic(const PagedAttnArgs& a, const PagedKernels& k) {
   auto* fn = paged_generic_kernel<DH, RB, KT>;
   static std::atomic<uint64_t> done{0};
   if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), G::smem, 0, &done, "medusa_paged_attn")) return rc;
-  launch_kernel(fn, dim3(k.sms * 2), dim3(kGenThreads), G::smem, k.stream, a);
+  launch_after(fn, dim3(k.sms * kGenCtas), dim3(kGenThreads), G::smem, k.stream, a);
   return check_launch("medusa_paged_attn");
 }
 
-size_t generic_part_bytes(int RB, int Dh, int sms) { return (size_t)(sms * 2) * 2 * (RB * Dh + 2 * RB) * 4; }
+size_t generic_part_bytes(int RB, int Dh, int sms) { return (size_t)(sms * kGenCtas) * 2 * (RB * Dh + 2 * RB) * 4; }
 
 // The workspace: both kernels' counters first, at the same place for every
 // size, then the rotated queries, then the partials.
@@ -403,22 +473,28 @@ bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows, int Dh, int b
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int launch_paged_prep(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, const PagedKernels& k) {
-  const int steps = (kPrepTokens * (a.H + 2 * a.Hkv) * (Dh / 16) + kPrepThreads - 1) / kPrepThreads;
-  const dim3 grid((a.total_q + kPrepTokens - 1) / kPrepTokens, (steps + 1) / 2);
-  if (dtype == MEDUSA_BF16) {
-    if (Dh == 64) launch_kernel(paged_prep_kernel<uint16_t, 64>, grid, dim3(kPrepThreads), 0, k.stream, a);
-    else launch_kernel(paged_prep_kernel<uint16_t, 128>, grid, dim3(kPrepThreads), 0, k.stream, a);
+namespace {
+template <typename T, int DH>
+int run_prep(const PagedAttnArgs& a, const PagedKernels& k) {
+  if (a.total_q >= 16 * 2 * k.sms) {  // two CTAs of 16 tokens for every SM
+    launch_kernel(paged_prep_kernel<T, DH, 16>, dim3((a.total_q + 15) / 16), dim3(kPrepThreads), 0, k.stream, a);
   } else {
-    if (Dh == 64) launch_kernel(paged_prep_kernel<float, 64>, grid, dim3(kPrepThreads), 0, k.stream, a);
-    else launch_kernel(paged_prep_kernel<float, 128>, grid, dim3(kPrepThreads), 0, k.stream, a);
+    const int per = kPrepThreads * kPrepSteps, items = 4 * (a.H + 2 * a.Hkv) * (DH / 16);
+    launch_kernel(paged_prep_kernel<T, DH, 4>, dim3((a.total_q + 3) / 4, (items + per - 1) / per), dim3(kPrepThreads),
+                  0, k.stream, a);
   }
   return check_launch("medusa_paged_attn");
+}
+}  // namespace
+
+int launch_paged_prep(const PagedAttnArgs& a, int Dh, medusa_dtype dtype, const PagedKernels& k) {
+  if (dtype == MEDUSA_BF16) return Dh == 64 ? run_prep<uint16_t, 64>(a, k) : run_prep<uint16_t, 128>(a, k);
+  return Dh == 64 ? run_prep<float, 64>(a, k) : run_prep<float, 128>(a, k);
 }
 
 int launch_paged_generic(const PagedAttnArgs& a, int Dh, bool few_rows, const PagedKernels& k) {
   if (few_rows) return Dh == 64 ? run_generic<64, 16, 64>(a, k) : run_generic<128, 16, 64>(a, k);
-  return Dh == 64 ? run_generic<64, 64, 32>(a, k) : run_generic<128, 64, 32>(a, k);
+  return Dh == 64 ? run_generic<64, 64, 64>(a, k) : run_generic<128, 64, 32>(a, k);
 }
 
 }  // namespace medusa

@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     if (warp == kLoadWarp && any) {
       // ------------------------------------------------ keys and values
-      asm volatile("fence.proxy.async.global;\n" ::: "memory");  // the appended tokens, written by the launch before
+      // the appended tokens, written by the launch before
+      asm volatile("griddepcontrol.wait;\n\tfence.proxy.async.global;\n" ::: "memory");
       const int box = min(a.p.page_size, KT), runs = KT / box;
       const int op_run = lane / G::kHalves, op_half = lane % G::kHalves;
       const bool mine = op_run < runs;
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // one ahead of its softmax, which keeps its registers for scores; lane
       // 0's warp also loads the segment's queries
       const int i = warp - kMmaWarp - 1;
+      asm volatile("griddepcontrol.wait;\n\tfence.proxy.async.global;\n" ::: "memory");
       int ns = 0;
       for (;; ++ns) {
         if (lane == 0) segs[i * 2 + (ns & 1)] = sg;
@@ -726,7 +728,7 @@ int run(const PagedAttnArgs& a, const PagedKernels& k) {
   // the registers' redistribution would wait for ever if the block had fewer to give
   if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), Cfg<DH>::smem, kLaunchRegs, &done, "medusa_paged_attn"))
     return rc;
-  launch_kernel(fn, dim3(k.sms), dim3(kThreads), Cfg<DH>::smem, k.stream, tmQ, tmK, tmV, a);
+  launch_after(fn, dim3(k.sms), dim3(kThreads), Cfg<DH>::smem, k.stream, tmQ, tmK, tmV, a);
   return check_launch("medusa_paged_attn");
 }
 
