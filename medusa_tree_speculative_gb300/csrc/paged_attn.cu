@@ -442,6 +442,24 @@ PagedWorkspace workspace_of(int total_q, int H, int Dh, medusa_dtype dtype, int 
   return w;
 }
 
+// The fractions of a turn per position (theta < 1 may turn more than once),
+// kept for the thread's next call: 64 powers take as long as a launch.
+void fill_turns(uint64_t* turns, float theta, int Dh) {
+  static thread_local float last_theta = 0.f;
+  static thread_local int last_dh = 0;
+  static thread_local uint64_t last[64];
+  if (theta != last_theta || Dh != last_dh) {
+    for (int j = 0; j < Dh / 2; ++j) {
+      double f = std::pow((double)theta, -2.0 * j / (double)Dh) / 6.283185307179586476925;
+      f -= std::floor(f);
+      last[j] = (uint64_t)std::ldexp(f, 64);
+    }
+    last_theta = theta;
+    last_dh = Dh;
+  }
+  for (int j = 0; j < Dh / 2; ++j) turns[j] = last[j];
+}
+
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -469,6 +487,18 @@ bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows, int Dh, int b
   const cuuint32_t boxes[2] = {64, (cuuint32_t)box};
   const cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_lines_map(CUtensorMap* m, const void* base, int64_t rows, int Dh, int box) {
+  EncodeTiled enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(Dh / 64)};
+  const cuuint64_t strides[2] = {(cuuint64_t)Dh * 2, 128};
+  const cuuint32_t boxes[3] = {64, (cuuint32_t)box, (cuuint32_t)(Dh / 64)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, boxes, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -550,12 +580,7 @@ extern "C" int medusa_paged_attn(const void* q, int64_t q_stride, const void* k_
     a.T = tree->T; a.W = tree->W; a.K = tree->K; a.depth = tree->depth; a.anc = tree->anc_mask;
   }
   a.H = H; a.Hkv = Hkv; a.g = H / Hkv;
-  for (int j = 0; j < Dh / 2; ++j) {
-    // the fraction of a turn per position; theta < 1 may turn more than once
-    double f = std::pow((double)rope_theta, -2.0 * j / (double)Dh) / 6.283185307179586476925;
-    f -= std::floor(f);
-    a.turns[j] = (uint64_t)std::ldexp(f, 64);
-  }
+  fill_turns(a.turns, rope_theta, Dh);
   a.qscale = scale * kPagedLog2e;
   a.out = out;
   a.q_rot = ws + w.q_rot;

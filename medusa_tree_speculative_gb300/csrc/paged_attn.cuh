@@ -330,6 +330,8 @@ bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows, int Dh, int b
 inline bool make_pool_map(CUtensorMap* m, const void* pool, const PagedAttnArgs& a, int Dh, int box) {
   return make_rows_map(m, pool, (int64_t)a.p.num_pages * a.Hkv * a.p.page_size, Dh, box);
 }
+// The same in boxes of all halves: [Dh / 64][box rows][64 values].
+bool make_lines_map(CUtensorMap* m, const void* base, int64_t rows, int Dh, int box);
 size_t paged_decode_part_bytes(int Dh, int sms);
 int launch_paged_decode(const PagedAttnArgs& a, int Dh, const PagedKernels& k);
 size_t paged_chunk_part_bytes(int Dh, int sms);

@@ -7,8 +7,8 @@
 // One CTA per SM holds six warps:
 //   * the load warp brings tiles of 64 keys and values into a ring of stages
 //     (160 KB, about 3.5 us of the SM's share of the memory's rate) by TMA, a
-//     lane per (page, 64-column half, pool), and runs on over the segments of
-//     the CTA's list;
+//     lane per (page, pool), both 64-column halves of a line in one copy, and
+//     runs on over the segments of the CTA's list;
 //   * the query warp rotates the next segment's query rows while the present
 //     one runs (two buffers).  Queries are kept as two bf16 parts, high and
 //     low, and multiplied in two MMAs: the tensor cores have time to spare
@@ -19,8 +19,14 @@
 // Before the loads of a tile that holds new tokens, the CTA itself (the only
 // one with that tile of that key head) rotates and appends them: no separate
 // launch.
+// Small calls are bound by latency.  Where every row's pages hold few tiles and
+// there are SMs to spare, a cluster of CL CTAs takes a unit instead: no list to
+// plan, and the join goes through distributed shared memory in place of the
+// workspace and its counters (one token at a prefix of 1024, 32 heads: 9.1 us
+// against 14.5).
 // P, unlike the queries, is rounded once to bf16 (a relative 2^-8 a weight,
 // independent from key to key).
+#include "cluster.cuh"
 #include "paged_attn.cuh"
 #include "sm100.cuh"
 
@@ -37,7 +43,6 @@ template <int DH>
 struct Cfg {
   static constexpr int kStages = DH == 128 ? 5 : 10;
   static constexpr uint32_t kTile = KT * DH * 2;                  // one pool's tile
-  static constexpr uint32_t kHalf = KT * 128;                     // its 64-column half
   static constexpr uint32_t kRing = kStages * 2 * kTile;
   static constexpr int kQStride = DH * 2 + 16;                    // bytes of a query row (padded: no bank conflicts)
   static constexpr uint32_t kQOff = kRing;                        // [2 buffers][high, low][16 rows]
@@ -56,6 +61,15 @@ struct Cfg {
 };
 
 MDEV void bar_consumers() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
+
+// Lines y .. of a pool, both halves: a box of [halves][lines][64 values].
+MDEV void tma_load_lines(void* dst, const CUtensorMap* map, uint64_t* bar, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %3}], [%2];\n" ::
+          "r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(y)
+      : "memory");
+}
 
 // The new tokens of a segment that lie in its tiles, rotated and written to
 // their pages by one warp.
@@ -86,7 +100,7 @@ MDEV void append_tokens(const PagedAttnArgs& a, const Segment& g, int lane) {
   }
 }
 
-template <int DH>
+template <int DH, int CL>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ PagedAttnArgs a) {
@@ -123,18 +137,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // rows past a segment's own keep whatever was here before: finite numbers
   for (uint32_t e = tid; e < G::kQBytes / 4; e += kThreads) reinterpret_cast<uint32_t*>(smem + G::kQOff)[e] = 0u;
-  int64_t x0, x1;
-  make_plan<kThreads, RB, KT, kCost>(a, sc, pl, x0, x1);
-  const int64_t total = pl.total, grid = min((int64_t)gridDim.x, total);
+  int64_t x1 = 0, total = 0, grid = 0;
   Segment sg;
-  const bool any = x0 < x1 && seek_segment<RB, KT, kCost>(a, sc, x0, x1, sg);
-  __syncthreads();  // the scratch becomes the warps' results
+  bool any;
+  if constexpr (CL == 1) {
+    int64_t x0;
+    make_plan<kThreads, RB, KT, kCost>(a, sc, pl, x0, x1);
+    total = pl.total;
+    grid = min((int64_t)gridDim.x, total);
+    any = x0 < x1 && seek_segment<RB, KT, kCost>(a, sc, x0, x1, sg);
+    __syncthreads();  // the scratch becomes the warps' results
+  } else {
+    // a cluster per unit, which is all of a sequence's rows of a key head
+    const int unit = blockIdx.x / CL, rank = (int)cluster_rank();
+    sg.b = unit / a.Hkv;
+    sg.head = unit - sg.b * a.Hkv;
+    sg.u = 0;
+    sg.m = 1;
+    sg.unit_x = 0;
+    int code;
+    bool ok = seq_info(a, sg.b, sg.s, code), twice = false;
+    if (a.rows && ok)
+      for (int j = tid; j < sg.b; j += kThreads) twice |= a.rows[j] == sg.s.row && a.q_start[j + 1] > a.q_start[j];
+    if (__syncthreads_or(twice)) {
+      ok = false;
+      code = MEDUSA_DEVERR_ROW;
+    }
+    if (code && sg.head == 0 && rank == 0 && tid == 0) set_err(a.err, code);
+    if (!ok) return;  // the whole cluster
+    sg.tiles = (sg.s.L + sg.s.n + KT - 1) / KT;
+    sg.t0 = (int)((int64_t)rank * sg.tiles / CL);
+    sg.t1 = (int)((int64_t)(rank + 1) * sg.tiles / CL);
+    any = sg.t0 < sg.t1;
+  }
+  auto next = [&](Segment& g) {
+    if constexpr (CL == 1) return next_segment<RB, KT, kCost>(a, pl, x1, g);
+    else return false;
+  };
+  // a cluster's join: every CTA's (max, sum) and sums of its tiles, at these
+  // places (the queries are in registers by then)
+  float* join = reinterpret_cast<float*>(smem + G::kQOff);
+  float2* join_ml = reinterpret_cast<float2*>(smem + G::kQOff + RB * G::kOStride * 4);
+  if constexpr (CL > 1) {
+    static_assert(RB * G::kOStride * 4 + RB * 8 <= G::kQBytes, "the join's place");
+    if (!any && tid < RB) join_ml[tid] = make_float2(-INFINITY, 0.f);
+  }
   if (any) {
     if (warp == 4) {
       // ------------------------------------------------ loads
       const int box = min(a.p.page_size, KT), runs = KT / box;  // runs of keys in one page each
-      const int op_run = lane >> 2, op_half = lane & 1, op_v = lane >> 1 & 1;
-      const bool mine = op_run < runs && op_half < DH / 64;
+      const int op_run = lane >> 1, op_v = lane & 1;
+      const bool mine = op_run < runs;
       const int nowhere = a.p.num_pages * a.Hkv << a.p.shift;  // past the pool: reads zeros
       const CUtensorMap* map = op_v ? &tmV : &tmK;
       bool told = false;
@@ -159,10 +212,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_expect_tx(&full[st], 2 * G::kTile);
           __syncwarp();
           if (mine)
-            tma_load_2d(smem + st * 2 * G::kTile + op_v * G::kTile + op_half * G::kHalf + op_run * box * 128, map,
-                        &full[st], op_half * 64, y);
+            tma_load_lines(smem + st * 2 * G::kTile + op_v * G::kTile + op_run * box * DH * 2, map, &full[st], y);
         }
-        if (!next_segment<RB, KT, kCost>(a, pl, x1, sg)) break;
+        if (!next(sg)) break;
       }
       // the copies in flight land before the CTA can end, whatever happened
       for (int j = max(0, it - G::kStages); j < it; ++j)
@@ -199,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) segs[bf] = sg;
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[bf]);
-        if (!next_segment<RB, KT, kCost>(a, pl, x1, sg)) break;
+        if (!next(sg)) break;
       }
     } else {
       // ------------------------------------------------ append, then attend
@@ -209,11 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         Segment g = sg;
         do {  // segments in turn to the four warps
           if ((n++ & 3) == warp && g.t1 * KT > g.s.L) append_tokens<DH>(a, g, lane);
-        } while (next_segment<RB, KT, kCost>(a, pl, x1, g));
+        } while (next(g));
         segments = n;
         asm volatile("fence.proxy.async.global;\n" ::: "memory");  // the tiles' loads read them back
         mbar_arrive(appended);
       }
+      // a tile in shared memory: runs of `box` keys, each [halves][box][128 bytes]
+      const int box = min(a.p.page_size, KT);
+      const uint32_t half = box * 128, first = (warp * 16 / box) * box * DH * 2 + (warp * 16 % box) * 128;
       const int r0 = lane >> 2, r1 = r0 + 8, kc = (lane & 3) * 2;  // this thread's rows and key columns
       int it = 0;
       for (int n = 0; n < segments; ++n) {
@@ -241,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = g.t0; t < g.t1; ++t, ++it) {
           const int st = it % G::kStages;
           paged_wait(&full[st], (uint32_t)(it / G::kStages) & 1u, abort_flag);
-          const uint32_t kb = sbase + st * 2 * G::kTile + warp * 16 * 128, vb = kb + G::kTile;
+          const uint32_t kb = sbase + st * 2 * G::kTile + first, vb = kb + G::kTile;
           float z[2][4] = {};
           {
             const int row = (lane & 7) + (lane >> 4) * 8, ch = lane >> 3 & 1;
@@ -249,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < DH / 16; ++kk) {
               const int c = kk * 2 + ch;
               uint32_t b[4];
-              ldmatrix_x4(b, kb + (c >> 3) * G::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+              ldmatrix_x4(b, kb + (c >> 3) * half + row * 128 + (((c & 7) ^ (row & 7)) << 4));
               mma_bf16_16816(z[0], qh[kk], b[0], b[1]);
               mma_bf16_16816(z[1], qh[kk], b[2], b[3]);
               mma_bf16_16816(z[0], ql[kk], b[0], b[1]);
@@ -311,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < DH / 16; ++j) {
             const int c = j * 2 + ch;
             uint32_t b[4];
-            ldmatrix_x4_trans(b, vb + (c >> 3) * G::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+            ldmatrix_x4_trans(b, vb + (c >> 3) * half + row * 128 + (((c & 7) ^ (row & 7)) << 4));
             if (edge) {
               b[0] &= keep0;
               b[1] &= keep1;
@@ -373,11 +428,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint2*>(dst + 32 * k) = make_uint2(pack2_bf16(acc[k][0] * inv, acc[k][1] * inv),
                                                                  pack2_bf16(acc[k][2] * inv, acc[k][3] * inv));
         };
-        if (g.t0 == 0 && g.t1 == g.tiles) {
+        if constexpr (CL > 1) {
+#pragma unroll
+          for (int k = 0; k < DH / 32; ++k)
+            *reinterpret_cast<float4*>(join + r * G::kOStride + c0 + 32 * k) =
+                make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+          if ((tid & 7) == 0) join_ml[r] = make_float2(M, sum);
+        } else if (g.t0 == 0 && g.t1 == g.tiles) {
           put();
         } else {
-          int first, last;
-          unit_shares<kCost>(g, total, grid, first, last);
+          int c_first, c_last;
+          unit_shares<kCost>(g, total, grid, c_first, c_last);
           float* mine = a.part + (int64_t)part_slot(g.unit_x, blockIdx.x, total, grid) * G::part_floats;
           if (r < live) {
 #pragma unroll
@@ -388,9 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           bar_consumers();
           if (tid == 0) {
-            const int before = arrive_acq_rel(a.counters + first);
-            *s_flag = before == last - first;
-            if (before == last - first) a.counters[first] = 0;  // ready for the next call
+            const int before = arrive_acq_rel(a.counters + c_first);
+            *s_flag = before == c_last - c_first;
+            if (before == c_last - c_first) a.counters[c_first] = 0;  // ready for the next call
           }
           bar_consumers();
           if (*s_flag && r < live) {
@@ -398,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum = 0.f;
 #pragma unroll
             for (int k = 0; k < DH / 32; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
-            for (int c = first; c <= last; ++c) {
+            for (int c = c_first; c <= c_last; ++c) {
               const float* pt = a.part + (int64_t)part_slot(g.unit_x, c, total, grid) * G::part_floats;
               const float2 e = __ldcg(reinterpret_cast<const float2*>(pt + RB * DH + 2 * r));
               float4 v[DH / 32];
@@ -422,28 +483,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  __syncthreads();
+  if constexpr (CL > 1) {
+    __syncwarp();
+    cluster_sync();  // every CTA's part is in place
+    constexpr int CW = DH / CL, kPer = CW / 4;  // this CTA's columns, four per thread
+    const int live = sg.s.n * a.g, rank = (int)cluster_rank();
+    for (int e = tid; e < live * kPer; e += kThreads) {
+      const int r = e / kPer, col = rank * CW + e % kPer * 4;
+      float2 ml[CL];
+      float4 v[CL];
+#pragma unroll
+      for (int c = 0; c < CL; ++c) {
+        ml[c] = ld_cluster_f2(cluster_map(smem_u32(join_ml + r), (uint32_t)c));
+        v[c] = ld_cluster_f4(cluster_map(smem_u32(join + r * G::kOStride + col), (uint32_t)c));
+      }
+      float M = -INFINITY, sum = 0.f, acc[4] = {};
+#pragma unroll
+      for (int c = 0; c < CL; ++c) M = fmaxf(M, ml[c].x);
+#pragma unroll
+      for (int c = 0; c < CL; ++c) {
+        if (ml[c].x == -INFINITY) continue;  // no tiles: nothing was written
+        const float f = exp2f(ml[c].x - M);
+        sum += f * ml[c].y;
+        acc[0] += f * v[c].x;
+        acc[1] += f * v[c].y;
+        acc[2] += f * v[c].z;
+        acc[3] += f * v[c].w;
+      }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const int i = r / a.g;
+      uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                      ((int64_t)(sg.s.q0 + i) * a.H + (int64_t)sg.head * a.g + r - i * a.g) * DH + col;
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack2_bf16(acc[0] * inv, acc[1] * inv), pack2_bf16(acc[2] * inv, acc[3] * inv));
+    }
+    __syncwarp();
+    cluster_sync();  // nobody leaves while its part may still be read
+  } else {
+    __syncthreads();
+  }
   if (tid == 0 && *abort_flag) set_err(a.err, MEDUSA_DEVERR_TIMEOUT);
 }
 
-template <int DH>
+template <int DH, int CL>
 int run(const PagedAttnArgs& a, const PagedKernels& k) {
   CUtensorMap tmK, tmV;
   const int box = a.p.page_size < KT ? a.p.page_size : KT;
-  if (!make_pool_map(&tmK, a.k_pages, a, DH, box) || !make_pool_map(&tmV, a.v_pages, a, DH, box))
+  const int64_t lines = (int64_t)a.p.num_pages * a.Hkv * a.p.page_size;
+  if (!make_lines_map(&tmK, a.k_pages, lines, DH, box) || !make_lines_map(&tmV, a.v_pages, lines, DH, box))
     return fail(MEDUSA_ERR_CUDA, "medusa_paged_attn: cuTensorMapEncodeTiled failed");
-  auto* fn = paged_decode_kernel<DH>;
+  auto* fn = paged_decode_kernel<DH, CL>;
   static std::atomic<uint64_t> done{0};
   if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), Cfg<DH>::smem, 0, &done, "medusa_paged_attn")) return rc;
-  launch_kernel(fn, dim3(k.sms), dim3(kThreads), Cfg<DH>::smem, k.stream, tmK, tmV, a);
+  if (CL == 1) launch_kernel(fn, dim3(k.sms), dim3(kThreads), Cfg<DH>::smem, k.stream, tmK, tmV, a);
+  else launch_cluster(fn, CL, dim3(a.B * a.Hkv * CL), dim3(kThreads), Cfg<DH>::smem, k.stream, tmK, tmV, a);
   return check_launch("medusa_paged_attn");
+}
+
+// The cluster that takes a unit (1: the shared list): as large as the SMs
+// allow, where the longest row that the cache can hold leaves a CTA at most
+// kClusterTiles tiles.
+constexpr int kClusterTiles = 16;
+template <int DH>
+int run_any(const PagedAttnArgs& a, const PagedKernels& k) {
+  const int64_t units = (int64_t)a.B * a.Hkv, tiles = ((int64_t)a.p.max_pages * a.p.page_size + KT - 1) / KT;
+  const int cl = units * 8 <= k.sms ? 8 : units * 4 <= k.sms ? 4 : units * 2 <= k.sms ? 2 : 1;
+  if (cl > 1 && tiles <= (int64_t)kClusterTiles * cl) {
+    if (cl == 8) return run<DH, 8>(a, k);
+    return cl == 4 ? run<DH, 4>(a, k) : run<DH, 2>(a, k);
+  }
+  return run<DH, 1>(a, k);
 }
 
 }  // namespace
 
 size_t paged_decode_part_bytes(int Dh, int sms) { return (size_t)sms * 2 * (RB * Dh + 2 * RB) * 4; }
 int launch_paged_decode(const PagedAttnArgs& a, int Dh, const PagedKernels& k) {
-  return Dh == 64 ? run<64>(a, k) : run<128>(a, k);
+  return Dh == 64 ? run_any<64>(a, k) : run_any<128>(a, k);
 }
 
 }  // namespace medusa
