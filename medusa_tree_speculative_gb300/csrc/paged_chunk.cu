@@ -57,13 +57,16 @@ struct Half {
   static constexpr uint32_t value = B;
 };
 
-template <int DH>
+// NARROW: a call whose chunks all have one query tile (at most 128 rows per key
+// head), bound by memory: the second tile's place goes to the ring.
+template <int DH, bool NARROW>
 struct Cfg {
   static constexpr int kHalves = DH / 64;
   static constexpr uint32_t kHalf = 128 * 128;          // 128 rows of one swizzle span
   static constexpr uint32_t kTile = kHalf * kHalves;    // 128 rows x DH bf16
-  static constexpr int kStages = 2;  // each the values of a tile and the keys of the next: one wait for both
-  static constexpr uint32_t kRingOff = 2 * kTile;
+  // a stage: the values of a tile and the keys of the next, one wait for both
+  static constexpr int kStages = !NARROW ? 2 : DH == 128 ? 3 : 6;
+  static constexpr uint32_t kRingOff = (NARROW ? 1 : 2) * kTile;
   static constexpr uint32_t kBarOff = kRingOff + kStages * 2 * kTile;
   static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 1 + 1 + 1;
   static constexpr uint32_t kSegOff = (kBarOff + kBars * 8 + 16 + 15) & ~15u;    // [2 lanes][2] segments
@@ -139,12 +142,30 @@ MDEV void umma_ts_const(uint32_t add) {
       "n"(A), "n"(B), "n"(IDESC), "r"(add)
       : "memory");
 }
+// The same from words known at run time (both descriptors' high words are the
+// same).
+MDEV void umma_words(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 A, B;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 A, {%1, %3};\n\tmov.b64 B, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], A, B, %4, p;\n\t}\n" ::"r"(d),
+      "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(add)
+      : "memory");
+}
+MDEV void umma_ts_words(uint32_t d, uint32_t a, uint32_t blo, uint32_t hi, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 B;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 B, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], B, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(blo), "r"(hi), "r"(idesc), "r"(add)
+      : "memory");
+}
 // The products of lane I with the keys or values in stage B (QT: the query
 // tile).  Matrix descriptors: 128-byte swizzle, 1024 bytes between 8-row
 // groups; low word address / 16 and, for V, the bytes / 16 between its halves.
 template <int DH>
 struct Products {
-  using G = Cfg<DH>;
+  using G = Cfg<DH, false>;
   static constexpr uint64_t kHi = (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32;
   static constexpr uint32_t kHalf16 = G::kHalf >> 4, kTile16 = G::kTile >> 4;
   static constexpr uint32_t kQ = kSmemBase >> 4 | 1u << 16, kK = (kSmemBase + G::kRingOff) >> 4 | 1u << 16;
@@ -197,11 +218,11 @@ MDEV void wait_at(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   *abort_flag = 1;
 }
 
-template <int DH>
+template <int DH, bool NARROW>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedAttnArgs a) {
-  using G = Cfg<DH>;
+  using G = Cfg<DH, NARROW>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase != kSmemBase) {
@@ -268,8 +289,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int op_run = lane / G::kHalves, op_half = lane % G::kHalves;
       const bool mine = op_run < runs;
       const int nowhere = (a.p.num_pages * a.Hkv) << a.p.shift;  // past the pool: reads zeros
-      // stage n (n & 1): the values of the CTA's tile n - 1, the keys of tile n
-      int n = 0, yv = 0;
+      // fill n of the ring: the values of the CTA's tile n - 1, the keys of tile n
+      int n = 0, yv = 0, st = 0;
+      uint32_t ph = 1;
       bool more = true;
       int t = sg.t0;
       while (true) {
@@ -283,8 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             else set_err(a.err, MEDUSA_DEVERR_PAGE);
           }
         }
-        const int st = n & 1;
-        paged_wait(&empty[st], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag);
+        paged_wait(&empty[st], ph, abort_flag);
         if (lane == 0) mbar_expect_tx(&full[st], (more ? G::kTile : 0u) + (n > 0 ? G::kTile : 0u));
         __syncwarp();
         uint8_t* dst = smem + G::kRingOff + st * 2 * G::kTile + op_half * G::kHalf + op_run * box * 128;
@@ -292,6 +313,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mine && more) tma_load_2d(dst, &tmK, &full[st], op_half * 64, y);
         yv = y;
         ++n;
+        if (++st == G::kStages) {
+          st = 0;
+          ph ^= 1u;
+        }
         if (!more) break;
         if (++t == sg.t1) {
           more = next_segment<RB, KT, kCost>(a, pl, x1, sg);
@@ -299,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // the copies in flight land before the CTA can end, whatever happened
-      for (int j = max(0, n - 2); j < n; ++j)
-        if (!mbar_wait(&full[j & 1], (uint32_t)(j >> 1) & 1u)) *abort_flag = 1;
+      for (int j = max(0, n - G::kStages); j < n; ++j)
+        if (!mbar_wait(&full[j % G::kStages], (uint32_t)(j / G::kStages) & 1u)) *abort_flag = 1;
     } else if (warp == kMmaWarp && any) {
       // ------------------------------------------------ MMAs
       // One thread issues 32 products' instructions per tile of 2048 cycles.
@@ -309,11 +334,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       // cycles even where it is over: so addresses are constants, and there are
       // as few waits and commits as will do (QK(j+1)'s commit also says that
       // PV(j), issued before it, is done).
-      if (elect_one()) {
+      constexpr uint32_t bars = kSmemBase + G::kBarOff;
+      constexpr uint32_t kEmpty = bars + G::kStages * 8, kS = kEmpty + G::kStages * 8, kP = kS + 2 * 8, kPV = kP + 2 * 8,
+                         kQ = kPV + 2 * 8, kQE = kQ + 8, kDone = kQE + 8;
+      if (NARROW) {
+        // Bound by memory: addresses at run time, a ring of more stages.  Lane
+        // j & 1 has tile j; QK runs two tiles ahead of PV, of the segment only.
+        if (elect_one()) {
+          constexpr uint32_t kStage16 = 2 * G::kTile >> 4, kHalf16 = G::kHalf >> 4, kTile16 = G::kTile >> 4;
+          constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+          constexpr uint32_t q16 = kSmemBase >> 4 | 1u << 16, k16 = (kSmemBase + G::kRingOff) >> 4 | 1u << 16;
+          constexpr uint32_t v16 = ((kSmemBase + G::kRingOff) >> 4) + kTile16 | kHalf16 << 16;
+          auto next_stage = [](uint32_t& st, uint32_t& ph) {
+            if (++st == G::kStages) {
+              st = 0;
+              ph ^= 1u;
+            }
+          };
+          uint32_t kst = 0, kph = 0;     // the stage with the next QK's keys
+          uint32_t vst = 0, vph = 0;     // ... with the next PV's values: the one after its keys'
+          next_stage(vst, vph);
+          uint32_t pph[2] = {0, 0}, qph = 0;
+          bool first = true, more = true;
+          auto scores = [&](uint32_t i) {
+            wait_at(bars + kst * 8, kph, abort_flag);
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk)
+              umma_words(i * 128, q16 + (kk >> 2) * kHalf16 + (kk & 3) * 2,
+                         k16 + kst * kStage16 + (kk >> 2) * kHalf16 + (kk & 3) * 2, kDescHi, idesc_bf16_f32(128, KT),
+                         kk != 0);
+            commit_at(kS + i * 8);
+            commit_at(kEmpty + kst * 8);
+            if (first) commit_at(kEmpty + kst * 8);  // the first stage has no values
+            first = false;
+            next_stage(kst, kph);
+          };
+          do {
+            const uint32_t n = sg.t1 - sg.t0;
+            wait_at(kQ, qph, abort_flag);
+            qph ^= 1u;
+            scores(0);
+            if (n > 1) scores(1);
+            if (n <= 2) commit_at(kQE);
+            for (uint32_t j = 0; j < n; ++j) {
+              const uint32_t i = j & 1u;
+              wait_at(bars + vst * 8, vph, abort_flag);
+              wait_at(kP + i * 8, pph[i], abort_flag);
+              pph[i] ^= 1u;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < KT / 16; ++k)
+                umma_ts_words(256 + i * 128, i * 128 + k * 8, v16 + vst * kStage16 + k * (2048 >> 4), kDescHi,
+                              idesc_bf16_f32(128, DH) | 1u << 16, k == 0 ? (uint32_t)(j > 1) : 1u);
+              commit_at(kEmpty + vst * 8);
+              next_stage(vst, vph);
+              if (j + 2 < n) {
+                scores(i);
+                if (j + 3 == n) commit_at(kQE);
+              } else {
+                commit_at(kPV + i * 8);
+              }
+            }
+            more = next_segment<RB, KT, kCost>(a, pl, x1, sg);
+          } while (more);
+          commit_at(kDone);
+          wait_at(kDone, 0, abort_flag);
+        }
+      } else if (elect_one()) {
         using P = Products<DH>;
-        constexpr uint32_t bars = kSmemBase + G::kBarOff;
-        constexpr uint32_t kEmpty = bars + 2 * 8, kS = bars + 4 * 8, kP = bars + 6 * 8, kPV = bars + 8 * 8,
-                           kQ = bars + 10 * 8, kQE = bars + 11 * 8, kDone = bars + 12 * 8;
         uint32_t t = 0, ph0 = 0, ph1 = 0, qph = 0;  // the CTA's tiles so far; phases of p_full and q_full
         uint32_t nt = sg.t1 - sg.t0, wide = min(tb, sg.s.n - sg.u * tb) * a.g > 128;
         bool ready = false;  // the segment's first scores are on their way
@@ -465,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Segment& g = segs[i * 2 + (ns & 1)];
         const int nt = g.t1 - g.t0, L = g.s.L, nkeys = L + g.s.n, tok0 = g.u * tb;
         const int live = min(tb, g.s.n - tok0) * a.g;
-        const bool wide = live > 128;
+        const bool wide = !NARROW && live > 128;
         const int row = wide ? i * 128 + r : r;
         const bool on = row < live;
         const int tok = min(tok0 + row / a.g, g.s.n - 1);
@@ -565,12 +654,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           // value rows past the sequence hold whatever the page does: zeros
           // (lane 0's P is waited for before either lane's product)
           if (key_base + (j + 1) * KT > nkeys && (i == 0 || !wide)) {
-            const int n = it + j + 1;  // the values' stage
-            paged_wait(&full[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
+            const int n = it + j + 1, st = n % G::kStages;  // the values' fill and stage
+            paged_wait(&full[st], (uint32_t)(n / G::kStages) & 1u, abort_flag);
             if (key_base + j * KT + r >= nkeys) {
 #pragma unroll
               for (int c = 0; c < G::kHalves * 8; ++c)
-                *reinterpret_cast<uint4*>(smem + G::kRingOff + (n & 1) * 2 * G::kTile + G::kTile + (c >> 3) * G::kHalf +
+                *reinterpret_cast<uint4*>(smem + G::kRingOff + st * 2 * G::kTile + G::kTile + (c >> 3) * G::kHalf +
                                           r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_smem_async();
@@ -716,19 +805,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && *abort_flag) set_err(a.err, MEDUSA_DEVERR_TIMEOUT);
 }
 
-template <int DH>
+template <int DH, bool NARROW>
 int run(const PagedAttnArgs& a, const PagedKernels& k) {
   CUtensorMap tmQ, tmK, tmV;
   const int box = a.p.page_size < KT ? a.p.page_size : KT;
   if (!make_rows_map(&tmQ, a.q_rot, (int64_t)a.total_q * a.H, DH, 128) ||
       !make_pool_map(&tmK, a.k_pages, a, DH, box) || !make_pool_map(&tmV, a.v_pages, a, DH, box))
     return fail(MEDUSA_ERR_CUDA, "medusa_paged_attn: cuTensorMapEncodeTiled failed");
-  auto* fn = paged_chunk_kernel<DH>;
+  auto* fn = paged_chunk_kernel<DH, NARROW>;
   static std::atomic<uint64_t> done{0};
   // the registers' redistribution would wait for ever if the block had fewer to give
-  if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), Cfg<DH>::smem, kLaunchRegs, &done, "medusa_paged_attn"))
+  if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), Cfg<DH, NARROW>::smem, kLaunchRegs, &done, "medusa_paged_attn"))
     return rc;
-  launch_after(fn, dim3(k.sms), dim3(kThreads), Cfg<DH>::smem, k.stream, tmQ, tmK, tmV, a);
+  launch_after(fn, dim3(k.sms), dim3(kThreads), Cfg<DH, NARROW>::smem, k.stream, tmQ, tmK, tmV, a);
   return check_launch("medusa_paged_attn");
 }
 
@@ -736,7 +825,8 @@ int run(const PagedAttnArgs& a, const PagedKernels& k) {
 
 size_t paged_chunk_part_bytes(int Dh, int sms) { return (size_t)sms * 4 * (128 * Dh + 2 * 128) * 4; }
 int launch_paged_chunk(const PagedAttnArgs& a, int Dh, const PagedKernels& k) {
-  return Dh == 64 ? run<64>(a, k) : run<128>(a, k);
+  if ((int64_t)a.max_new * a.g <= 128) return Dh == 64 ? run<64, true>(a, k) : run<128, true>(a, k);
+  return Dh == 64 ? run<64, false>(a, k) : run<128, false>(a, k);
 }
 
 }  // namespace medusa
