@@ -765,26 +765,31 @@ __global__ void __launch_bounds__(kThreads, 1)
               M = N;
             }
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            constexpr int kCols = DH == 128 ? 64 : 32;  // a partial's columns in flight
 #pragma unroll 1
-            for (int c = c0; c < c1; c += 16) {
-              float acc[16];
+            for (int c = c0; c < c1; c += kCols) {
+              float acc[kCols];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+              for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
               for (int k = first; k <= last; ++k) {
                 const float* pt = part(k);
                 const float pm = __ldcg(pt + 128 * DH + 2 * r);
+                float4 f[kCols / 4];
+#pragma unroll
+                for (int e = 0; e < kCols / 4; ++e)
+                  f[e] = __ldcg(reinterpret_cast<const float4*>(pt + ((c / 4 + e) * 128 + r) * 4));
                 if (pm == -INFINITY) continue;
                 const float w = ex2(pm - M);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 f = __ldcg(reinterpret_cast<const float4*>(pt + ((c / 4 + e) * 128 + r) * 4));
-                  acc[4 * e] += w * f.x;
-                  acc[4 * e + 1] += w * f.y;
-                  acc[4 * e + 2] += w * f.z;
-                  acc[4 * e + 3] += w * f.w;
+                for (int e = 0; e < kCols / 4; ++e) {
+                  acc[4 * e] += w * f[e].x;
+                  acc[4 * e + 1] += w * f[e].y;
+                  acc[4 * e + 2] += w * f[e].z;
+                  acc[4 * e + 3] += w * f[e].w;
                 }
               }
-              put(c, acc, inv);
+#pragma unroll
+              for (int e = 0; e < kCols; e += 16) put(c + e, acc + e, inv);
             }
           }
           __syncwarp();
