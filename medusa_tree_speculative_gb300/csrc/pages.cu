@@ -293,12 +293,16 @@ __global__ void __launch_bounds__(kBlock) pages_commit_kernel(PagesDev p, const 
 }
 
 // The plan of a compaction, one CTA: with n live pages, the i-th live page at
-// or past n goes to the i-th free page below n.  work[0] = n, or -1 where
-// nothing moves; work[16 + page] = where a moved page went.
-__global__ void __launch_bounds__(kBlock) pages_plan_kernel(PagesDev p, int32_t* copies, int max_copies,
-                                                            int32_t* n_copies, int32_t* work, int32_t* err) {
+// or past n goes to the i-th free page below n.  It leaves n (or -1 where
+// nothing moves) in work[0], and a PlanWord per word of the bit map at work + 16.
+struct alignas(16) PlanWord {
+  uint32_t out, hole;            // live pages past n, free pages below n
+  int32_t outs_before, holes_before;
+};
+
+__global__ void __launch_bounds__(kBlock) pages_plan_kernel(PagesDev p, int max_copies, int32_t* n_copies,
+                                                            int32_t* work, int32_t* err) {
   __shared__ uint64_t sums[33];
-  __shared__ uint64_t base[kBlock];
   const int t = threadIdx.x;
   const int words = (p.num_pages + 31) / 32, per = (words + kBlock - 1) / kBlock;
   uint64_t live = 0, total;
@@ -325,9 +329,8 @@ __global__ void __launch_bounds__(kBlock) pages_plan_kernel(PagesDev p, int32_t*
     split(w, out, hole);
     mine += (uint64_t)__popc(out) << 32 | (uint64_t)__popc(hole);
   }
-  base[t] = block_exclusive_sum(mine, sums, total);
+  uint64_t at = block_exclusive_sum(mine, sums, total);
   const int moves = (int)(total >> 32);
-  __syncthreads();
   if (moves > max_copies) {  // nothing changes
     if (t == 0) {
       *n_copies = 0;
@@ -336,47 +339,79 @@ __global__ void __launch_bounds__(kBlock) pages_plan_kernel(PagesDev p, int32_t*
     }
     return;
   }
-  const int lane = t & 31;
-  const uint32_t before = (1u << lane) - 1u;
-  for (int c = t >> 5; c < kBlock && c * per < words; c += 32) {
-    int at_out = (int)(base[c] >> 32), at_hole = (int)(uint32_t)base[c];
-    for (int k = 0; k < per && c * per + k < words; ++k) {
-      uint32_t out, hole;
-      split(c * per + k, out, hole);
-      const int page = (c * per + k) * 32 + lane;
-      if (out >> lane & 1u) copies[4 * (int64_t)(at_out + __popc(out & before))] = page;
-      if (hole >> lane & 1u) copies[4 * (int64_t)(at_hole + __popc(hole & before)) + 1] = page;
-      at_out += __popc(out);
-      at_hole += __popc(hole);
-    }
+  PlanWord* plan = reinterpret_cast<PlanWord*>(work + 16);
+  for (int k = 0; k < per; ++k) {
+    const int w = t * per + k;
+    if (w >= words) break;
+    PlanWord x;
+    split(w, x.out, x.hole);
+    x.outs_before = (int)(at >> 32);
+    x.holes_before = (int)(uint32_t)at;
+    plan[w] = x;
+    at += (uint64_t)__popc(x.out) << 32 | (uint64_t)__popc(x.hole);
+    p.free_bits[w] = live_word_mask(w, p.num_pages) & ~low_mask(w);
   }
-  __syncthreads();  // the list is complete, and nobody reads free_bits any more
-  for (int i = t; i < moves; i += kBlock) {
-    int4 e = *reinterpret_cast<const int4*>(copies + 4 * (int64_t)i);
-    e.z = p.page_size;
-    e.w = -1;
-    *reinterpret_cast<int4*>(copies + 4 * (int64_t)i) = e;
-    work[16 + e.x] = e.y;
-    p.refs[e.y] = p.refs[e.x];
-    p.refs[e.x] = 0;
-  }
-  for (int w = t; w < words; w += kBlock) p.free_bits[w] = live_word_mask(w, p.num_pages) & ~low_mask(w);
   if (t == 0) {
     *n_copies = moves;
     work[0] = moves > 0 ? n : -1;
   }
 }
 
-// The table after the plan: a CTA per row.
-__global__ void __launch_bounds__(256) pages_retable_kernel(PagesDev p, const int32_t* work, int32_t* err) {
-  const int n = work[0];
+// The i-th free page below n, from the last word with at most i such pages
+// before it.
+MDEV int nth_hole(const PlanWord* plan, int words, int i) {
+  int lo = 0, hi = words - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (plan[mid].holes_before <= i) lo = mid; else hi = mid - 1;
+  }
+  uint32_t bits = plan[lo].hole;
+  int nth = i - plan[lo].holes_before, at = 0;
+#pragma unroll
+  for (int half = 16; half > 0; half >>= 1) {  // the nth set bit, by halves
+    const int below = __popc(bits & ((1u << half) - 1u));
+    if (nth >= below) {
+      nth -= below;
+      bits >>= half;
+      at += half;
+    }
+  }
+  return lo * 32 + at;
+}
+
+// The rest of it: a CTA per row brings the table in line with the plan, and the
+// CTAs behind those write the list and move the reference counts, a thread per
+// page.  (One CTA that writes the list too takes 35 us for 16384 moves of 65536
+// pages, bound by its own issue and scattered stores.)
+__global__ void __launch_bounds__(256) pages_move_kernel(PagesDev p, const int32_t* work, int32_t* copies,
+                                                         int32_t* err) {
+  const int n = work[0], words = (p.num_pages + 31) / 32;
   if (n < 0) return;
-  const int r = blockIdx.x, held = min(max(p.held[r], 0), p.max_pages);
-  int32_t* row = p.table + (int64_t)r * p.max_pages;
-  for (int c = threadIdx.x; c < held; c += blockDim.x) {
-    const int page = row[c];
-    if (!page_ok(p, page)) set_err(err, MEDUSA_DEVERR_PAGE);
-    else if (page >= n) row[c] = work[16 + page];
+  const PlanWord* plan = reinterpret_cast<const PlanWord*>(work + 16);
+  auto moves_to = [&](int page, int& i) {  // where a page goes (-1: it is free); i = its line in the list
+    const PlanWord x = plan[page >> 5];
+    if (!(x.out >> (page & 31) & 1u)) return -1;
+    i = x.outs_before + __popc(x.out & ((1u << (page & 31)) - 1u));
+    return nth_hole(plan, words, i);
+  };
+  int i;
+  if ((int)blockIdx.x < p.rows) {
+    const int r = blockIdx.x, held = min(max(p.held[r], 0), p.max_pages);
+    int32_t* row = p.table + (int64_t)r * p.max_pages;
+    for (int c = threadIdx.x; c < held; c += blockDim.x) {
+      const int page = row[c], to = page_ok(p, page) && page >= n ? moves_to(page, i) : page;
+      if (!page_ok(p, to)) set_err(err, MEDUSA_DEVERR_PAGE);
+      else if (to != page) row[c] = to;
+    }
+    return;
+  }
+  const int step = (gridDim.x - p.rows) * blockDim.x;
+  for (int page = n + (blockIdx.x - p.rows) * blockDim.x + threadIdx.x; page < p.num_pages; page += step) {
+    const int to = moves_to(page, i);
+    if (to < 0) continue;
+    *reinterpret_cast<int4*>(copies + 4 * (int64_t)i) = make_int4(page, to, p.page_size, -1);
+    p.refs[to] = p.refs[page];
+    p.refs[page] = 0;
   }
 }
 
@@ -569,7 +604,7 @@ extern "C" int medusa_pages_commit(const medusa_pages_t* pages, const int32_t* r
 }
 
 extern "C" size_t medusa_pages_compact_workspace_size(int num_pages) {
-  return num_pages < 1 ? 0 : align_up((size_t)(16 + (size_t)num_pages) * 4, 256);
+  return num_pages < 1 ? 0 : align_up(64 + (((size_t)num_pages + 31) / 32) * sizeof(PlanWord), 256);
 }
 
 extern "C" int medusa_pages_compact(const medusa_pages_t* pages, int32_t* copies, int max_copies, int32_t* n_copies,
@@ -579,14 +614,16 @@ extern "C" int medusa_pages_compact(const medusa_pages_t* pages, int32_t* copies
   if (!copies || !n_copies) return fail(MEDUSA_ERR_INVALID, "%s: NULL copies or n_copies", fn);
   if (max_copies < 0) return fail(MEDUSA_ERR_INVALID, "%s: max_copies=%d", fn, max_copies);
   if (reinterpret_cast<uintptr_t>(copies) % 16) return fail(MEDUSA_ERR_INVALID, "%s: copies not 16-byte aligned", fn);
+  if (reinterpret_cast<uintptr_t>(workspace) % 16)
+    return fail(MEDUSA_ERR_INVALID, "%s: workspace not 16-byte aligned", fn);
   if (!workspace || workspace_bytes < medusa_pages_compact_workspace_size(pages->num_pages))
     return fail(MEDUSA_ERR_WORKSPACE, "%s: workspace of %zu bytes is too small", fn, workspace_bytes);
   const PagesDev p = pages_dev(pages);
   auto* work = static_cast<int32_t*>(workspace);
-  launch_kernel(pages_plan_kernel, dim3(1), dim3(kBlock), 0, as_stream(stream), p, copies, max_copies, n_copies, work,
-                err);
+  launch_kernel(pages_plan_kernel, dim3(1), dim3(kBlock), 0, as_stream(stream), p, max_copies, n_copies, work, err);
   if (int rc = check_launch(fn)) return rc;
-  launch_kernel(pages_retable_kernel, dim3(pages->rows), dim3(256), 0, as_stream(stream), p, work, err);
+  const int blocks = (pages->num_pages + 255) / 256, movers = blocks < 2 * sm_count() ? blocks : 2 * sm_count();
+  launch_kernel(pages_move_kernel, dim3(pages->rows + movers), dim3(256), 0, as_stream(stream), p, work, copies, err);
   return check_launch(fn);
 }
 
