@@ -723,7 +723,8 @@ size_t medusa_paged_attn_workspace_size(int B, int total_q, int max_new, int H,
  * a turn at any position.  The cache is read as it is stored, in its type.
  * A key that a token does not see has no effect on it, with one limit:
  * non-finite values among a chunk's own v_new may reach other tokens of the
- * same chunk.
+ * same chunk.  A token that sees a NaN score gets NaN, one whose scores are all
+ * minus infinity gets zeros.
  * length stays (medusa_pages_commit); the pages for L + n_b tokens must be
  * there and the last ones the row's own (medusa_pages_reserve).
  * out: device [total_q][H][Dh].  H a multiple of Hkv, H / Hkv <= 64, Dh 64 or

@@ -332,13 +332,15 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
     if (live <= 16) tiles(std::integral_constant<int, 1>());
     else tiles(std::integral_constant<int, G::TM>());
 #pragma unroll
-    for (int i = 0; i < G::TM; ++i)
+    for (int i = 0; i < G::TM; ++i) {
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+      if (l[i] != l[i]) m[i] = INFINITY;  // so that no join drops a part whose scores are all NaN
+    }
     auto put = [&](int i, const float* v, float sum) {  // row ty + 16 i of the block
       const int r = ty + 16 * i;
       if (r >= live) return;
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       float* dst = static_cast<float*>(a.out) +
                ((int64_t)(s.q0 + tok0 + r / a.g) * a.H + (int64_t)sg.head * a.g + r % a.g) * DH;
 #pragma unroll

@@ -675,6 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           tc_fence_after();
         }
+        if (l != l) m = INFINITY;  // so that no join drops a part whose scores are all NaN
         // Two query tiles: a thread ends with its row.  One: the lanes' results
         // are joined, and it has half of the columns (both threads read the
         // same tensor-memory lane).
@@ -719,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            pack2_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
         };
         if (nt == g.tiles) {
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
           for (int c = c0; c < c1; c += 16) {
             float o[16];
@@ -764,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (N != -INFINITY) sum = sum * ex2(M - N) + e.y * ex2(e.x - N);
               M = N;
             }
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
             constexpr int kCols = DH == 128 ? 64 : 32;  // a partial's columns in flight
 #pragma unroll 1
             for (int c = c0; c < c1; c += kCols) {

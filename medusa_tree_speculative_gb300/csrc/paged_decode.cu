@@ -384,6 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           l0 += __shfl_xor_sync(0xffffffffu, l0, w);
           l1 += __shfl_xor_sync(0xffffffffu, l1, w);
         }
+        if (l0 != l0) m0 = INFINITY;  // so that no join drops a part whose scores are all NaN
+        if (l1 != l1) m1 = INFINITY;
         // the four warps' results joined: eight threads per row
         bar_consumers();  // the previous segment's are read
         float* ob = reinterpret_cast<float*>(smem + G::kOOff) + warp * RB * G::kOStride;
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         auto put = [&]() {
           if (r >= live) return;
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const int i = r / a.g;
           uint16_t* dst = static_cast<uint16_t*>(a.out) +
                           ((int64_t)(s.q0 + i) * a.H + (int64_t)g.head * a.g + r - i * a.g) * DH + c0;
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc[2] += f * v[c].z;
         acc[3] += f * v[c].w;
       }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const int i = r / a.g;
       uint16_t* dst = static_cast<uint16_t*>(a.out) +
                       ((int64_t)(sg.s.q0 + i) * a.H + (int64_t)sg.head * a.g + r - i * a.g) * DH + col;

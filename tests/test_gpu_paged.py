@@ -441,6 +441,95 @@ def test_page_outside_the_pool(M, dt, n):
     c.check(before, skip=(0,))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hkv,Dh", [(2, 2, 128), (4, 1, 64), (2, 1, 128)])
+@pytest.mark.parametrize("rows", [15, 16, 17, 127, 128, 129, 192])
+def test_rows_around_a_tile(M, dt, H, Hkv, Dh, rows):
+    """Query rows per key head (tokens x shared heads) on both sides of a tile of 16 and of 128."""
+    n = max(1, rows // (H // Hkv))
+    Chunk(M, dt, H, Hkv, Dh, 32, [n, 1, n], [200, 0, 1500], gap=1, seed=rows).go()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,Hkv,L", [(1, 1, 0), (1, 1, 1), (1, 2, 4000), (2, 1, 65), (9, 2, 1000), (9, 4, 900),
+                                     (20, 4, 1500), (3, 8, 30000)])
+def test_decode_sequences_and_lengths(M, dt, B, Hkv, L):
+    """One token: few sequences, whose keys several CTAs share, to many; one much longer than the rest."""
+    Chunk(M, dt, 4 * Hkv, Hkv, 128, 16, [1] * B, [L] + [L // 7 + b for b in range(B - 1)], seed=B).go()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_skipped_single_tokens(M, dt):
+    """As test_skipped_sequences, one token each."""
+    c = Chunk(M, dt, 4, 2, 128, 16, [1, 1, 1, 1, 0], [900, 50, 7, 33, 12], seed=15)
+    before = c.k.clone(), c.v.clone()
+    c.rows[3] = c.rows[1]
+    c.where = i32(c.rows)
+    c.pages.length[c.rows[2]] = -1
+    c.run()
+    torch.cuda.synchronize()
+    assert c.err.item() == ROW | PAGE
+    c.check(before, skip=(2, 3))
+    c = Chunk(M, dt, 4, 2, 128, 16, [1, 1, 1, 3, 0], [900, 50, 15, 33, 12], seed=16)
+    before = c.k.clone(), c.v.clone()
+    c.max_new = 2
+    c.pages.length[c.rows[2]] = 16  # no page for the next token
+    c.run()
+    torch.cuda.synchronize()
+    assert c.err.item() == LENGTH | CAPACITY
+    c.check(before, skip=(2, 3))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_nothing_to_do(M, dt):
+    """No sequences, no tokens, only sequences without tokens: nothing is written."""
+    c = Chunk(M, dt, 4, 2, 128, 16, [0, 0], [40, 0], gap=3, seed=17)
+    before = c.k.clone(), c.v.clone()
+    for max_new in (0, 1, 7, 300):
+        c.max_new = max_new
+        c.run()
+    c.q_start, c.where = i32([0]), i32([])
+    c.run()
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    c.check(before)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_long_batch_of_chunks(M, dt):
+    """Thousands of new tokens in one call, one of its rows named twice."""
+    c = Chunk(M, dt, 2, 1, 64, 64, [3000, 1, 2500, 700], [10, 77, 0, 129], gap=1, seed=18)
+    before = c.k.clone(), c.v.clone()
+    c.rows[3] = c.rows[0]
+    c.where = i32(c.rows)
+    c.run()
+    torch.cuda.synchronize()
+    assert c.err.item() == ROW
+    c.check(before, skip=(3,))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 20, 150])
+def test_non_finite_inputs_stay_where_they_are(M, dt, n):
+    """NaN and infinities in one token's query, in a key that earlier tokens do not see, and in another sequence's
+    values: every other output keeps its bits."""
+    c = Chunk(M, dt, 4, 2, 128, 16, [n, n, n], [300, 40, 700], seed=19)
+    c.run()
+    want, err = c.out.clone(), c.err.item()
+    assert err == 0
+    at = c.start[0] + n // 2
+    c.q[at] = float("nan")
+    c.kn[c.start[2] - 1] = float("inf")
+    c.vn[c.start[2] + n // 3] = float("-inf")
+    c.run()
+    torch.cuda.synchronize()
+    same = torch.ones(3 * n, dtype=torch.bool, device="cuda")
+    same[at] = same[c.start[2] - 1] = False
+    same[c.start[2]:] = False
+    assert torch.equal(c.out[same], want[same])
+    assert c.out[at].isnan().all() and not c.out[c.start[2] + n - 1].isfinite().any()
+
+
 # ------------------------------------------------------------ accepted path ---
 
 @pytest.mark.parametrize("dt,Hkv,Dh,ps", [("bf16", 4, 128, 16), ("f32", 2, 64, 32), ("bf16", 7, 64, 256)])
