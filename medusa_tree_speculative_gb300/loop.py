@@ -72,10 +72,12 @@ class StandInModel:
 
 
 class DecodeLoop:
-    """n_steps verify steps on the device, each fed by the previous one."""
+    """n_steps verify steps on the device, each fed by the previous one.  With
+    page_size the cache is paged: the sequences' tokens, the same as in the
+    dense slabs, lie in pages of that many tokens, taken as the steps need them."""
 
     def __init__(self, w: dict, model: StandInModel, tree: M.DeviceTree, n_steps: int, L0: int, x0,
-                 device="cuda", heads: str = "fused", seed: int = 0):
+                 device="cuda", heads: str = "fused", seed: int = 0, page_size: int | None = None):
         B, H, Dh, d, K = w["B"], w["H"], w["Dh"], w["d"], w["K"]
         assert H * Dh == d, "the stand-in takes q, k and v from the hidden rows"
         T = tree.T
@@ -91,16 +93,37 @@ class DecodeLoop:
             vc[b * cap:b * cap + L0] = torch.randn(L0, H, Dh, generator=g, device=device).to(dt)
         self.hidden = torch.zeros(B, T, d, dtype=dt, device=device)
         qkv = self.hidden.view(B, T, H, Dh)
-        self.st = S.VerifyStep(w, model.weights(), tree, max_prefix=cap - T, device=device, heads=heads)
-        self.x = {"q": qkv, "k_new": qkv, "v_new": qkv, "hidden": self.hidden, "tokens": self.st.next_tokens,
-                  "k_cache": kc, "v_cache": vc,
-                  "seq_start": torch.arange(B, dtype=torch.int64, device=device) * cap,
-                  "prefix_len": torch.full((B,), L0, dtype=torch.int32, device=device),
-                  "seq_cap": torch.full((B,), cap, dtype=torch.int64, device=device)}
+        self.st = S.VerifyStep(w, model.weights(), tree, max_prefix=cap - T, device=device, heads=heads,
+                               cache="paged" if page_size else "dense")
+        self.x = {"q": qkv, "k_new": qkv, "v_new": qkv, "hidden": self.hidden, "tokens": self.st.next_tokens}
+        if page_size:
+            self._into_pages(kc.view(B, cap, H, Dh), vc.view(B, cap, H, Dh), L0, cap, page_size)
+        else:
+            self.x.update({"k_cache": kc, "v_cache": vc,
+                           "seq_start": torch.arange(B, dtype=torch.int64, device=device) * cap,
+                           "prefix_len": torch.full((B,), L0, dtype=torch.int32, device=device),
+                           "seq_cap": torch.full((B,), cap, dtype=torch.int64, device=device)})
         self.out = torch.zeros(B, n_steps * (tree.K + 1) + 1, dtype=torch.int32, device=device)
         self.out_len = torch.zeros(B, dtype=torch.int32, device=device)
         self.x0 = np.asarray(x0, np.int64).reshape(B)
         self._prime()
+
+    def _into_pages(self, k, v, L0: int, cap: int, page_size: int):
+        """A paged cache whose rows hold the first L0 tokens of the slabs k, v [B][cap][H][Dh]."""
+        st, x, B = self.st, self.x, self.B
+        per = -(-cap // page_size)
+        pages = M.Pages(B, per, B * per, page_size)
+        pools = [torch.zeros(B * per, k.shape[2], page_size, k.shape[3], dtype=k.dtype, device=k.device)
+                 for _ in range(2)]
+        n0 = torch.full((B,), L0, dtype=torch.int32, device=k.device)
+        M.medusa_pages_reserve(pages, n0, st.copies, st.n_copies, None, st.err)
+        M.medusa_pages_commit(pages, None, n0, 0, st.err)
+        at = torch.arange(L0, device=k.device)
+        page = pages.table[:, at // page_size].long()  # [B][L0]
+        for pool, slab in zip(pools, (k, v)):
+            pool[page, :, at % page_size] = slab[:, :L0]
+        x.update({"k_pages": pools[0], "v_pages": pools[1], "pages": pages, "rows": None,
+                  "n_new": torch.full((B,), self.T, dtype=torch.int32, device=k.device)})
 
     def _prime(self):
         """The state before the first step: the root is next(x0) and the tree

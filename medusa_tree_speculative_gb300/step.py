@@ -13,6 +13,11 @@ for the next step):
   accepted node's row, or ("joint", bf16) medusa_lm_head_verify_heads_hidden
   in place of the LM head call (logits and every row's u in one pass) and
   then medusa_heads_logits_topk.
+
+With cache="paged" the keys and values lie in the pages of a medusa_pages_t
+instead of one slab per sequence: medusa_pages_reserve, medusa_pages_copy and
+medusa_paged_attn take the tree attention's place, medusa_paged_compact and
+medusa_pages_commit the compaction's.
 """
 from __future__ import annotations
 
@@ -65,7 +70,10 @@ class VerifyStep:
 
     def __init__(self, w: dict, weights: dict, tree: M.DeviceTree, max_prefix: int, device="cuda",
                  heads: str = "fused", accept: str = "separate", write_logits: bool = True,
-                 attn_order: str = "after_lm", attn_splits="auto"):
+                 attn_order: str = "after_lm", attn_splits="auto", cache: str = "dense"):
+        if cache not in ("dense", "paged"):
+            raise ValueError(f"cache {cache!r}")
+        self.cache = cache
         self.w, self.tree, self.max_prefix = w, tree, max_prefix
         # attention on the forked branch: enqueued before the LM head ("first"),
         # right after it ("after_lm": its CTAs then take the SMs the LM head
@@ -144,7 +152,15 @@ class VerifyStep:
         if self.accept == "fused":
             self.stat_groups = M.medusa_lm_head_stat_groups(B * T, V)
             self.stats = torch.zeros((self.stat_groups, B * T, 4), dtype=torch.float32, device=device)
-        self.ws_attn = ws(M.medusa_tree_attn_workspace_size(B, H, Dh, T, max_prefix))
+        if cache == "paged":  # its arrival counters: zero-filled once
+            self.Hkv = w.get("Hkv", H)
+            self.q_start = torch.arange(B + 1, **i32) * T
+            self.copies = torch.zeros((M.MAX_ROWS, 4), **i32)
+            self.n_copies = torch.zeros(1, **i32)
+            self.ws_attn = torch.zeros(M.medusa_paged_attn_workspace_size(B, B * T, T, H, self.Hkv, Dh, dt),
+                                       dtype=torch.uint8, device=device)
+        else:
+            self.ws_attn = ws(M.medusa_tree_attn_workspace_size(B, H, Dh, T, max_prefix))
         # the acceptance keeps per-sequence counters in its workspace: zero-filled once
         self.ws_accept = torch.zeros(max(256, M.medusa_accept_workspace_size(B, T)), dtype=torch.uint8,
                                      device=device)
@@ -172,6 +188,11 @@ class VerifyStep:
     def run(self, x: dict, stream=None, side_stream=None, heads_stream=None, append=None):
         """x: device tensors q, k_new, v_new, hidden, tokens, k_cache, v_cache,
         seq_start, prefix_len, seq_cap.  Updates the cache and prefix_len.
+        With cache="paged", instead of the last five: k_pages, v_pages, pages
+        (a Pages), rows (the sequences' rows [B], or None: row b) and n_new
+        ([pages.rows]: T for those rows, 0 for the others).  Updates the pools
+        and the pages' state; a row that gets no page sets err, keeps its
+        length and its `out` means nothing.
 
         One stream: tree attention, LM head, acceptance, heads, candidates,
         KV compaction.  With `side_stream`: the chain LM head -> acceptance ->
@@ -228,6 +249,11 @@ class VerifyStep:
             side.wait_stream(main)  # compaction needs the accepted path
 
         def compaction():
+            if self.cache == "paged":
+                M.medusa_paged_compact(x["k_pages"], x["v_pages"], x["pages"], x["rows"], self.accepted_nodes,
+                                       self.accept_len, self.T, self.err, side)
+                M.medusa_pages_commit(x["pages"], x["rows"], self.accept_len, 1, self.err, side)
+                return
             M.medusa_kv_compact(x["k_cache"], x["v_cache"], x["seq_start"], x["prefix_len"],
                                 self.accepted_nodes, self.accept_len, self.tree.K, self.tree.T, self.src_slots,
                                 self.err, side)
@@ -254,7 +280,16 @@ class VerifyStep:
 
     def attention(self, x: dict, stream):
         """The step's tree attention (box step 1) on `stream`."""
-        if self.attn_splits == "tc":
+        if self.cache == "paged":
+            B, T, H, Dh = self.out.shape
+            copies = self.copies[:x["pages"].rows]
+            M.medusa_pages_reserve(x["pages"], x["n_new"], copies, self.n_copies, None, self.err, stream)
+            M.medusa_pages_copy(x["k_pages"], x["v_pages"], copies, self.n_copies, self.err, stream)
+            M.medusa_paged_attn(x["q"].view(B * T, H, Dh), x["k_new"].view(B * T, self.Hkv, Dh),
+                                x["v_new"].view(B * T, self.Hkv, Dh), x["k_pages"], x["v_pages"], x["pages"],
+                                x["rows"], self.q_start, T, self.tree, self.rope_theta, self.scale,
+                                self.out.view(B * T, H, Dh), self.ws_attn, self.err, stream)
+        elif self.attn_splits == "tc":
             M.medusa_tree_attn_tc(x["q"], x["k_new"], x["v_new"], x["k_cache"], x["v_cache"], x["seq_start"],
                                   x["prefix_len"], x["seq_cap"], self.tree, self.max_prefix, self.rope_theta,
                                   self.scale, self.out, self.err, stream, key_splits=self.tc_splits)
@@ -268,6 +303,10 @@ class VerifyStep:
         """Kernels one run() launches: attention 1 (2 for f32), LM head 1,
         acceptance 1, compaction 1, heads 2 with the candidate fill ("fused"),
         or heads 2 ("split"; 1 "joint": W1 runs in the LM head's launch) and
-        candidates 1."""
+        candidates 1.  Paged: reserve, copy, attention 2 (1 up to 16 query rows
+        per key head), compaction 1, commit 1."""
         heads = {"fused": 2, "split": 3, "joint": 2}[self.heads]
+        if self.cache == "paged":
+            attn = 1 if self.T * (self.w["H"] // self.Hkv) <= 16 else 2
+            return 2 + attn + 1 + 1 + 2 + heads
         return (1 if self.w["dtype"] == "bf16" else 2) + 1 + 1 + 1 + heads
