@@ -222,10 +222,11 @@ MDEV bool set_tiles(Segment& g, int64_t x, int64_t x1) {
 }
 
 // The segment that place x of the list is in (x < x1); false if [x, x1) has no
-// tiles.
+// tiles.  Whole warps call it: a lane per block tried (a search by halves, each
+// step an Euclid of 64-bit divisions, took 8 us for 128 blocks).
 template <int RB, int KT, int EC>
 MDEV bool seek_segment(const PagedAttnArgs& a, const PlanScratch& sc, int64_t x, int64_t x1, Segment& g) {
-  const int tb = RB / a.g;
+  const int tb = RB / a.g, lane = threadIdx.x & 31;
   int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before x: it has places, or total would be x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -235,18 +236,23 @@ MDEV bool seek_segment(const PagedAttnArgs& a, const PlanScratch& sc, int64_t x,
   int code;
   seq_info(a, lo, g.s, code);
   g.m = (g.s.n + tb - 1) / tb;
-  const int64_t each = seq_places<KT, EC>(a, g.s, tb);
-  int64_t rest = x - sc.pre[lo];
+  const int64_t each = (sc.pre[lo + 1] - sc.pre[lo]) / a.Hkv;
+  int64_t rest = x - sc.pre[lo], before = 0;
   g.head = (int)(rest / each);
   rest -= (int64_t)g.head * each;
-  int ulo = 0, uhi = g.m - 1;
-  while (ulo < uhi) {
-    const int mid = (ulo + uhi + 1) >> 1;
-    if (places_before<KT, EC>(a, g.s, tb, mid) <= rest) ulo = mid; else uhi = mid - 1;
+  int u = 0, last = g.m - 1;  // the last block that starts at or before `rest`
+  while (u < last) {
+    const int step = (last - u + 31) >> 5, v = u + (lane + 1) * step;
+    int64_t at = 0;
+    if (v <= last) at = places_before<KT, EC>(a, g.s, tb, v);
+    const int k = __popc(__ballot_sync(0xffffffffu, v <= last && at <= rest));
+    if (k > 0) before = __shfl_sync(0xffffffffu, at, k - 1);
+    u += k * step;
+    last = min(last, u + step - 1);
   }
-  g.u = ulo;
-  rest -= places_before<KT, EC>(a, g.s, tb, ulo);
-  g.tiles = unit_tiles<KT>(a, g.s, tb, ulo);
+  g.u = u;
+  rest -= before;
+  g.tiles = unit_tiles<KT>(a, g.s, tb, u);
   g.unit_x = x - rest;
   return set_tiles<EC>(g, x, x1);
 }
