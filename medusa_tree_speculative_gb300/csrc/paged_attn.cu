@@ -15,9 +15,10 @@ namespace {
 // loads of kPrepSteps steps in flight.  Queries go to q_rot with the softmax
 // scale in them, keys and values to their pages.  Every element is read and
 // written once: bound by memory for long chunks (16 tokens per CTA, all heads:
-// 8192 tokens of 48 heads in XXX us), by the latency of a thread's few steps
+// 8192 tokens of 48 heads, 201 MB, in 37 us), by the latency of a thread's few steps
 // for short ones (4 tokens, as many groups of heads as give a thread
-// kPrepSteps).
+// kPrepSteps).  16 against 4 tokens per CTA, with the attention: 392 and 396 us
+// for 8192 tokens; 132 and 100 us for 260.
 constexpr int kPrepThreads = 256;
 constexpr int kPrepSteps = 4;
 
@@ -173,7 +174,15 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_c
 // its maximum and sum are four shuffles.  Key rows are padded by 16 bytes
 // (eight threads' 16-byte loads of eight rows then hit different banks).  The
 // value tile loads while S is computed and the next key tile while O is.
-constexpr int kGenThreads = 256, kGenCtas = 2;  // CTAs per SM
+// Bound by shared memory: a warp's sixteen products of four rows and four keys
+// need eight 16-byte loads, which take about as many cycles as 1.5 times the
+// products (the FMA pipe is 41% busy).  345 tokens in five sequences, 16 heads
+// of 64 (four per key head), prefixes up to 2000: 74 us with the rotation's
+// launch.  Blocks of at most 16 rows have a form of their own where the call
+// has no others: one token at a prefix of 1024, 32 heads of 128, 22.6 us against
+// 28.7 in the form for 64 rows; 64 tokens, 16 heads of 128 (four per key head),
+// prefixes up to 4000, 144 against 160.
+constexpr int kGenThreads = 256, kGenCtas = 2;  // CTAs per SM (the two cases above: 74 and 144 us; with 3: 89, 186)
 
 template <int DH, int RB, int KT>
 struct Gen {
@@ -207,22 +216,31 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
   while (true) {
     const SeqInfo& s = sg.s;
     const int nkeys = s.L + s.n, tok0 = sg.u * tb, live = min(tb, s.n - tok0) * a.g;
-    // one tile of keys or values, zeros where there is none
-    auto load = [&](const void* pool, float* dst, int stride, int t) {
-      constexpr int kRow = DH / 4;
-      for (int e = tid; e < KT * kRow; e += kGenThreads) {
-        const int key = t * KT + e / kRow, c = e % kRow;
-        const float* src = static_cast<const float*>(pool);
-        bool ok = key < nkeys;
-        if (ok) {
+    // The lines this thread copies of a tile (-1: none, zeros), looked up a
+    // tile ahead: a copy waits for no page number.
+    constexpr int kRow = DH / 4, kCopies = KT * kRow / kGenThreads;
+    int line[kCopies];
+    auto find = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        const int key = t * KT + (tid + i * kGenThreads) / kRow;
+        line[i] = -1;
+        if (t < sg.t1 && key < nkeys) {
           const int page = page_of(a, s, key);
-          ok = page >= 0;
-          if (ok) src += page_line(a.p, page, a.Hkv, sg.head, key & (a.p.page_size - 1)) * DH + c * 4;
+          if (page >= 0) line[i] = (int)page_line(a.p, page, a.Hkv, sg.head, key & (a.p.page_size - 1));
         }
-        cp_async16(smem_u32(dst + (e / kRow) * stride + c * 4), src, ok ? 16 : 0);
+      }
+    };
+    auto load = [&](const void* pool, float* dst, int stride) {
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        const int e = tid + i * kGenThreads, c = e % kRow;
+        cp_async16(smem_u32(dst + (e / kRow) * stride + c * 4),
+                   static_cast<const float*>(pool) + (int64_t)max(line[i], 0) * DH + c * 4, line[i] >= 0 ? 16 : 0);
       }
       cp_async_commit();
     };
+    find(sg.t0);
     __syncthreads();  // the previous segment's tiles are read
     {
       const float* qr = static_cast<const float*>(a.q_rot) +
@@ -234,8 +252,9 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
         store8(Qs + r * (DH + 4) + c * 8, f);
       }
     }
-    load(a.k_pages, Ks, DH + 4, sg.t0);
-    load(a.v_pages, Vs, DH, sg.t0);
+    load(a.k_pages, Ks, DH + 4);
+    load(a.v_pages, Vs, DH);
+    find(sg.t0 + 1);
     float o[G::TM][G::CC * 4], m[G::TM], l[G::TM];
 #pragma unroll
     for (int i = 0; i < G::TM; ++i) {
@@ -244,8 +263,10 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
 #pragma unroll
       for (int c = 0; c < G::CC * 4; ++c) o[i][c] = 0.f;
     }
-    // a block with at most 16 rows (a single token beside longer chunks) has
-    // them all in i = 0
+    // A block with at most 16 rows (a single token, alone or beside longer
+    // chunks) has them all in i = 0; the warps past its rows only copy, since
+    // every row costs shared memory's bandwidth, live or not.
+    const bool on = (tid >> 5) * 2 < live;
     auto tiles = [&](auto active) {
       constexpr int N = decltype(active)::value;
       for (int t = sg.t0; t < sg.t1; ++t) {
@@ -253,7 +274,7 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
         __syncthreads();
         float z[N][G::TN] = {};
 #pragma unroll 4
-        for (int d = 0; d < DH; d += 4) {
+        for (int d = 0; d < (on ? DH : 0); d += 4) {
           float4 qv[N], kv[G::TN];
 #pragma unroll
           for (int i = 0; i < N; ++i) qv[i] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * (DH + 4) + d);
@@ -266,11 +287,12 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
               z[i][j] += qv[i].x * kv[j].x + qv[i].y * kv[j].y + qv[i].z * kv[j].z + qv[i].w * kv[j].w;
         }
         __syncthreads();  // the keys are read
-        if (t + 1 < sg.t1) load(a.k_pages, Ks, DH + 4, t + 1);
+        if (t + 1 < sg.t1) load(a.k_pages, Ks, DH + 4);
         else cp_async_commit();
         const bool masked = (t + 1) * KT > s.L;  // keys past the prefix: the mask decides
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+          if (!on) break;
           const int r = ty + 16 * i, tok = tok0 + r / a.g;
           if (masked) {
 #pragma unroll
@@ -301,7 +323,7 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
         cp_async_wait<1>();  // this tile's values
         __syncthreads();
 #pragma unroll 2
-        for (int k = 0; k < KT; k += 4) {
+        for (int k = 0; k < (on ? KT : 0); k += 4) {
           float4 pv[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * (KT + 4) + k);
@@ -325,8 +347,9 @@ __global__ void __launch_bounds__(kGenThreads) paged_generic_kernel(const __grid
           }
         }
         __syncthreads();  // the values are read
-        if (t + 1 < sg.t1) load(a.v_pages, Vs, DH, t + 1);
+        if (t + 1 < sg.t1) load(a.v_pages, Vs, DH);
         else cp_async_commit();
+        find(t + 2);
       }
     };
     if (live <= 16) tiles(std::integral_constant<int, 1>());
@@ -590,8 +613,11 @@ extern "C" int medusa_paged_attn(const void* q, int64_t q_stride, const void* k_
   const PagedKernels k{as_stream(stream), sms};
   // One attention launch for the whole call, by its longest chunk.  A batch
   // with both kinds of sequences goes through the kernels for many rows: two
-  // launches, one per kind, took 130 us against 114 us for eleven sequences of
-  // 1 .. 700 tokens (40 heads of 64, prefixes up to 5000).
+  // launches, one per kind, took 14% longer for eleven sequences of 1 .. 700
+  // tokens (40 heads of 64, prefixes up to 5000).  Up to kFewRows rows per key
+  // head the kernels for few rows are ahead: 64 single tokens with four heads
+  // per key head and prefixes up to 8192 take 187 us, 205 us in the other one;
+  // one token at a prefix of 1024, 11.7 and 24.6 us.
   const bool few = (int64_t)max_new * a.g <= kFewRows;
   a.counters = reinterpret_cast<int*>(ws) + (few ? 0 : kPagedCounters);
   a.part = reinterpret_cast<float*>(ws + w.part);

@@ -101,6 +101,47 @@ def test_bookkeeping_random_rounds(M, rows, max_pages, num_pages, ps):
         assert (copies[len(moves):] == -7).all()
 
 
+def test_bookkeeping_of_a_large_pool(M):
+    """Several words of the bit map per thread, the last ones ragged; a compaction that moves thousands of pages."""
+    rng = random.Random(9)
+    rows, most, num, ps = 30, 9000, 200013, 16
+    c = Cache(M, rows, most, num, ps)
+    n_new = [rng.randint(0, most * ps) for _ in range(rows)]
+    c.reserve(n_new)
+    c.commit(None, n_new)
+    c.free([rng.choice([-1, -1, 0, rng.randint(0, n)]) for n in n_new])
+    moves = c.book.compact()
+    copies, n = i32([[-7] * 4] * (len(moves) + 1)), i32([-1])
+    ws = torch.empty(M.medusa_pages_compact_workspace_size(num), dtype=torch.uint8, device="cuda")
+    M.medusa_pages_compact(c.pages, copies, n, ws, c.err)
+    c.same()
+    assert len(moves) > 1000 and n.item() == len(moves) and copies.tolist() == moves + [[-7] * 4]
+    c.reserve([rng.randint(0, 40) for _ in range(rows)])
+
+
+def test_compact_with_a_table_that_names_free_pages(M):
+    """A row whose table names a free page past the live ones: PAGE, that entry stays, the others move."""
+    c = Cache(M, 3, 4, 64, 16)
+    c.reserve([64, 64, 64])
+    c.commit(None, [64, 64, 64])
+    c.free([0, -1, -1])
+    c.pages.table[1, 2] = 60
+    copies, n = i32([[-7] * 4] * 8), i32([-1])
+    ws = torch.empty(M.medusa_pages_compact_workspace_size(64), dtype=torch.uint8, device="cuda")
+    M.medusa_pages_compact(c.pages, copies, n, ws, c.err)
+    assert c.err.item() == PAGE and n.item() == 4
+    assert c.pages.table[1].tolist() == [4, 5, 60, 7] and c.pages.table[2].tolist() == [0, 1, 2, 3]
+
+
+def test_optional_outputs_may_be_left_out(M):
+    c = Cache(M, 2, 2, 3, 16)
+    M.medusa_pages_reserve(c.pages, i32([20, 40]), c.copies, c.n_copies)  # the second row does not fit
+    M.medusa_pages_commit(c.pages, None, i32([20, 1]))
+    M.medusa_pages_fork(c.pages, i32([0]), i32([5]))
+    M.medusa_pages_free(c.pages, i32([17, -1]))
+    assert c.pages.length.tolist() == [17, 0] and c.pages.held.tolist() == [2, 0]
+
+
 def test_every_row_shares_one_tail(M):
     """1024 rows on one partly filled page: all but the last sharer copy it, in row order."""
     c = Cache(M, 1024, 2, 1100, 16)
@@ -528,6 +569,71 @@ def test_non_finite_inputs_stay_where_they_are(M, dt, n):
     same[c.start[2]:] = False
     assert torch.equal(c.out[same], want[same])
     assert c.out[at].isnan().all() and not c.out[c.start[2] + n - 1].isfinite().any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 70])
+def test_rows_left_out(M, dt, n):
+    """rows = None is row b for sequence b, in a cache with more rows."""
+    c = Chunk(M, dt, 4, 2, 64, 16, [n, n, 1], [33, 500, 20], seed=20, shuffle=False)
+    c.go()
+    want = c.out.clone()
+    big = M.Pages(9, c.pages.max_pages, c.pages.num_pages, 16)
+    for f in ("refs", "free_bits"):
+        getattr(big, f).copy_(getattr(c.pages, f))
+    for f in ("length", "held", "table"):
+        getattr(big, f)[:3] = getattr(c.pages, f)
+    c.pages, c.where = big, None
+    c.out.fill_(7.0)
+    c.run()
+    torch.cuda.synchronize()
+    assert c.err.item() == 0 and torch.equal(c.out, want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 5])
+def test_many_heads(M, dt, n):
+    Chunk(M, dt, 300, 300, 64, 16, [n, 0, n], [70, 9, 3], seed=21).go()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_room_for_much_more(M, dt):
+    """Rows whose tables reach far past what they hold."""
+    for n, L in (([1, 1], [100, 3]), ([30, 1], [100, 3])):
+        c = Chunk(M, dt, 8, 2, 128, 16, n, L, seed=22)
+        before = c.k.clone(), c.v.clone()
+        p = M.Pages(c.pages.rows, 70000, c.pages.num_pages, 16)
+        for f in ("refs", "free_bits", "length", "held"):
+            getattr(p, f).copy_(getattr(c.pages, f))
+        p.table[:, :c.pages.max_pages] = c.pages.table
+        c.pages = p
+        c.run()
+        torch.cuda.synchronize()
+        assert c.err.item() == 0
+        c.check(before)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_graphs_that_share_a_workspace(M, dt):
+    """Two captured calls of different kinds with one workspace, replayed in turn on one stream."""
+    a = Chunk(M, dt, 8, 2, 128, 16, [1, 1, 1], [3000, 17, 900], seed=23)
+    b = Chunk(M, dt, 8, 2, 128, 16, [200, 1, 90], [300, 17, 900], seed=24)
+    a.ws = b.ws
+    want, graphs = [], []
+    for c in (a, b):
+        c.go()
+        want.append(c.out.clone())
+        g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            c.run()
+        graphs.append(g)
+    for _ in range(4):
+        for c, g, w in zip((a, b), graphs, want):
+            c.out.fill_(7.0)
+            g.replay()
+            assert torch.equal(c.out, w)
+    assert a.err.item() == 0 and b.err.item() == 0
 
 
 # ------------------------------------------------------------ accepted path ---
