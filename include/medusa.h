@@ -604,6 +604,7 @@ int medusa_standin_embed(const int32_t* tokens, int rows, const void* emb,
  *
  * A decode step of a batch:
  *   medusa_pages_reserve   room for each row's new tokens; its list of copies
+ *   medusa_pages_served    the batch without the rows that got none
  *   medusa_pages_copy      ... carried out, once per layer
  *   medusa_paged_attn      once per layer: append, attend
  *   medusa_paged_compact   once per layer, after a tree: the accepted path
@@ -662,6 +663,15 @@ int medusa_pages_fork(const medusa_pages_t* pages, const int32_t* src,
 int medusa_pages_reserve(const medusa_pages_t* pages, const int32_t* n_new,
                          int32_t* copies, int max_copies, int32_t* n_copies,
                          int32_t* granted, int32_t* err, void* stream);
+
+/* served[b] = rows[b] (rows NULL: b) where granted (medusa_pages_reserve's)
+ * says that the row has its room, else -1, b < B: as `rows` of the calls below
+ * it makes them skip the sequences without room (MEDUSA_DEVERR_ROW), which
+ * would otherwise write into pages that they may share.  rows, served: device
+ * [B]; granted: device [pages->rows]. */
+int medusa_pages_served(const medusa_pages_t* pages, const int32_t* rows,
+                        const int32_t* granted, int B, int32_t* served,
+                        void* stream);
 
 /* length[rows[b]] += n_new[b] + bias for b < B (rows, n_new: device [B]; rows
  * NULL: row b).  After a chunk bias is 0; after a verified tree n_new is

@@ -264,6 +264,14 @@ __global__ void __launch_bounds__(kBlock) pages_reserve_kernel(PagesDev p, const
   }
 }
 
+__global__ void __launch_bounds__(kBlock) pages_served_kernel(PagesDev p, const int32_t* rows, const int32_t* granted,
+                                                              int B, int32_t* served) {
+  const int b = threadIdx.x;
+  if (b >= B) return;
+  const int r = rows ? rows[b] : b;
+  served[b] = (unsigned)r < (unsigned)p.rows && granted[r] != 0 ? r : -1;
+}
+
 // Thread b is entry b of the batch; a row named twice counts once.
 __global__ void __launch_bounds__(kBlock) pages_commit_kernel(PagesDev p, const int32_t* rows, const int32_t* n_new,
                                                               int bias, int B, int32_t* err) {
@@ -589,6 +597,19 @@ extern "C" int medusa_pages_reserve(const medusa_pages_t* pages, const int32_t* 
                 pages->rows);
   launch_kernel(pages_reserve_kernel, dim3(1), dim3(kBlock), 0, as_stream(stream), pages_dev(pages), n_new, copies,
                 n_copies, granted, err);
+  return check_launch(fn);
+}
+
+extern "C" int medusa_pages_served(const medusa_pages_t* pages, const int32_t* rows, const int32_t* granted, int B,
+                                   int32_t* served, void* stream) {
+  const char* fn = "medusa_pages_served";
+  if (int rc = check_pages(pages, fn)) return rc;
+  if (B < 0 || B > MEDUSA_MAX_ROWS || (!rows && B > pages->rows))
+    return fail(MEDUSA_ERR_INVALID, "%s: B=%d for %d rows", fn, B, pages->rows);
+  if (B == 0) return MEDUSA_OK;
+  if (!granted || !served) return fail(MEDUSA_ERR_INVALID, "%s: NULL granted or served", fn);
+  launch_kernel(pages_served_kernel, dim3(1), dim3(kBlock), 0, as_stream(stream), pages_dev(pages), rows, granted, B,
+                served);
   return check_launch(fn);
 }
 

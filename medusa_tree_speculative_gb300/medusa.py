@@ -87,6 +87,7 @@ _SIGS = {
     "medusa_pages_free": (I, [PAGES, P, P, P]),
     "medusa_pages_fork": (I, [PAGES, P, P, I, P, P]),
     "medusa_pages_reserve": (I, [PAGES, P, P, I, P, P, P, P]),
+    "medusa_pages_served": (I, [PAGES, P, P, I, P, P]),
     "medusa_pages_commit": (I, [PAGES, P, P, I, I, P, P]),
     "medusa_pages_compact_workspace_size": (SZ, [I]),
     "medusa_pages_compact": (I, [PAGES, P, I, P, P, SZ, P, P]),
@@ -617,6 +618,13 @@ def medusa_pages_reserve(pages: Pages, n_new, copies, n_copies, granted=None, er
                                      _lines(copies), _ints(n_copies, "n_copies", d, 1),
                                      _ints(granted, "granted", d, pages.rows), _ints(err, "err", d),
                                      _launch_on(stream, d)), "medusa_pages_reserve")
+
+
+def medusa_pages_served(pages: Pages, rows, granted, served, stream=None):
+    """served[b] = rows[b] (rows None: b) where granted (medusa_pages_reserve's) is set, else -1."""
+    d, B = pages.index, served.numel()
+    _check(_lib.medusa_pages_served(pages.ref, _ints(rows, "rows", d, B), _ints(granted, "granted", d, pages.rows), B,
+                                    _ints(served, "served", d), _launch_on(stream, d)), "medusa_pages_served")
 
 
 def medusa_pages_commit(pages: Pages, rows, n_new, bias: int = 0, err=None, stream=None):

@@ -15,9 +15,9 @@ for the next step):
   then medusa_heads_logits_topk.
 
 With cache="paged" the keys and values lie in the pages of a medusa_pages_t
-instead of one slab per sequence: medusa_pages_reserve, medusa_pages_copy and
-medusa_paged_attn take the tree attention's place, medusa_paged_compact and
-medusa_pages_commit the compaction's.
+instead of one slab per sequence: medusa_pages_reserve, medusa_pages_served,
+medusa_pages_copy and medusa_paged_attn take the tree attention's place,
+medusa_paged_compact and medusa_pages_commit the compaction's.
 """
 from __future__ import annotations
 
@@ -157,6 +157,8 @@ class VerifyStep:
             self.q_start = torch.arange(B + 1, **i32) * T
             self.copies = torch.zeros((M.MAX_ROWS, 4), **i32)
             self.n_copies = torch.zeros(1, **i32)
+            self.granted = torch.zeros(M.MAX_ROWS, **i32)
+            self.served = torch.zeros(B, **i32)  # the sequences' rows, -1 for those without room
             self.ws_attn = torch.zeros(M.medusa_paged_attn_workspace_size(B, B * T, T, H, self.Hkv, Dh, dt),
                                        dtype=torch.uint8, device=device)
         else:
@@ -191,8 +193,9 @@ class VerifyStep:
         With cache="paged", instead of the last five: k_pages, v_pages, pages
         (a Pages), rows (the sequences' rows [B], or None: row b) and n_new
         ([pages.rows]: T for those rows, 0 for the others).  Updates the pools
-        and the pages' state; a row that gets no page sets err, keeps its
-        length and its `out` means nothing.
+        and the pages' state; a sequence that the pool has no room for sets
+        err and is skipped: no output, its cache and length as they were, -1
+        in `served`.
 
         One stream: tree attention, LM head, acceptance, heads, candidates,
         KV compaction.  With `side_stream`: the chain LM head -> acceptance ->
@@ -250,9 +253,9 @@ class VerifyStep:
 
         def compaction():
             if self.cache == "paged":
-                M.medusa_paged_compact(x["k_pages"], x["v_pages"], x["pages"], x["rows"], self.accepted_nodes,
+                M.medusa_paged_compact(x["k_pages"], x["v_pages"], x["pages"], self.served, self.accepted_nodes,
                                        self.accept_len, self.T, self.err, side)
-                M.medusa_pages_commit(x["pages"], x["rows"], self.accept_len, 1, self.err, side)
+                M.medusa_pages_commit(x["pages"], self.served, self.accept_len, 1, self.err, side)
                 return
             M.medusa_kv_compact(x["k_cache"], x["v_cache"], x["seq_start"], x["prefix_len"],
                                 self.accepted_nodes, self.accept_len, self.tree.K, self.tree.T, self.src_slots,
@@ -282,12 +285,13 @@ class VerifyStep:
         """The step's tree attention (box step 1) on `stream`."""
         if self.cache == "paged":
             B, T, H, Dh = self.out.shape
-            copies = self.copies[:x["pages"].rows]
-            M.medusa_pages_reserve(x["pages"], x["n_new"], copies, self.n_copies, None, self.err, stream)
+            copies, granted = self.copies[:x["pages"].rows], self.granted[:x["pages"].rows]
+            M.medusa_pages_reserve(x["pages"], x["n_new"], copies, self.n_copies, granted, self.err, stream)
+            M.medusa_pages_served(x["pages"], x["rows"], granted, self.served, stream)
             M.medusa_pages_copy(x["k_pages"], x["v_pages"], copies, self.n_copies, self.err, stream)
             M.medusa_paged_attn(x["q"].view(B * T, H, Dh), x["k_new"].view(B * T, self.Hkv, Dh),
                                 x["v_new"].view(B * T, self.Hkv, Dh), x["k_pages"], x["v_pages"], x["pages"],
-                                x["rows"], self.q_start, T, self.tree, self.rope_theta, self.scale,
+                                self.served, self.q_start, T, self.tree, self.rope_theta, self.scale,
                                 self.out.view(B * T, H, Dh), self.ws_attn, self.err, stream)
         elif self.attn_splits == "tc":
             M.medusa_tree_attn_tc(x["q"], x["k_new"], x["v_new"], x["k_cache"], x["v_cache"], x["seq_start"],
@@ -303,10 +307,10 @@ class VerifyStep:
         """Kernels one run() launches: attention 1 (2 for f32), LM head 1,
         acceptance 1, compaction 1, heads 2 with the candidate fill ("fused"),
         or heads 2 ("split"; 1 "joint": W1 runs in the LM head's launch) and
-        candidates 1.  Paged: reserve, copy, attention 2 (1 up to 16 query rows
-        per key head), compaction 1, commit 1."""
+        candidates 1.  Paged: reserve, served, copy, attention 2 (1 up to 16
+        query rows per key head), compaction 1, commit 1."""
         heads = {"fused": 2, "split": 3, "joint": 2}[self.heads]
         if self.cache == "paged":
             attn = 1 if self.T * (self.w["H"] // self.Hkv) <= 16 else 2
-            return 2 + attn + 1 + 1 + 2 + heads
+            return 3 + attn + 1 + 1 + 2 + heads
         return (1 if self.w["dtype"] == "bf16" else 2) + 1 + 1 + 1 + heads

@@ -135,3 +135,41 @@ def test_loop_on_pages(M, name, B, ps, graph):
         assert torch.equal(paged.x["v_pages"][page, :, i % ps], both[0].x["v_cache"][b * cap:b * cap + L])
     refs = pages.refs.cpu()
     assert int(refs.sum()) == int(pages.held.sum()) and refs.max() == 1
+
+
+@pytest.mark.parametrize("name,ps", [("tiny_fp32", 16), ("tiny_bf16", 16)])
+def test_step_without_room(M, name, ps):
+    """Three sequences, pages for one tree: the first goes on, the others, which share a tail page that their trees
+    would begin in, are skipped whole."""
+    from medusa_tree_speculative_gb300 import step
+
+    L = 21
+    w = dict(workloads.get(name), B=3, L=(L, L, L))
+    tree = M.DeviceTree(step.build_tree(w))
+    T, H, Dh = tree.T, w["H"], w["Dh"]
+    x = {k: to_dev(v) for k, v in synth.make_step(w, T, 5).items()}
+    wts = {k: (None if v is None else to_dev(v)) for k, v in synth.make_weights(w, 5).items()}
+    new = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    st = step.VerifyStep(w, wts, tree, max_prefix=L, cache="paged")
+    assert 2 * ps < L + T <= 3 * ps  # each row needs one more page, the sharers a copy of their tail as well
+    pages = M.Pages(4, 8, 5, ps)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    pools = [torch.randn(5, H, ps, Dh, generator=g, device="cuda").to(x["k_cache"].dtype) for _ in range(2)]
+    M.medusa_pages_reserve(pages, new([L, L, 0, 0]), st.copies, st.n_copies, None, st.err)
+    M.medusa_pages_commit(pages, None, new([L, L, 0, 0]), 0, st.err)
+    M.medusa_pages_fork(pages, new([1]), new([3]), st.err)
+    before = pages.state.clone(), [p.clone() for p in pools]
+    st.out.fill_(7.0)
+    st.run(dict(x, k_pages=pools[0], v_pages=pools[1], pages=pages, rows=new([0, 3, 1]), n_new=new([T, T, 0, T])))
+    torch.cuda.synchronize()
+    assert st.err.item() == 4 | 64  # capacity, and rows that are skipped
+    assert st.served.tolist() == [0, -1, -1]
+    assert pages.length.tolist() == [L + 1 + int(st.accept_len[0]), L, 0, L]
+    assert (st.out[1:] == 7.0).all() and not (st.out[0] == 7.0).any()
+    others = torch.ones(5, dtype=torch.bool, device="cuda")
+    others[pages.table[0, :3].long()] = False
+    assert int(others.sum()) == 2
+    for p, q in zip(pools, before[1]):
+        assert torch.equal(p[others], q[others])
+    old = M.Pages.from_state(before[0], 4, 8, 5, ps)
+    assert torch.equal(pages.table[1:], old.table[1:]) and torch.equal(pages.held[1:], old.held[1:])

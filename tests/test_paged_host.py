@@ -53,6 +53,11 @@ def test_bookkeeping_refusals(M):
     assert L.medusa_pages_reserve(p, None, FAKE, 4, FAKE, None, None, None) == -1
     assert L.medusa_pages_reserve(p, FAKE, FAKE + 4, 4, FAKE, None, None, None) == -1
     assert L.medusa_pages_reserve(p, FAKE, FAKE, 3, FAKE, None, None, None) == -3
+    assert L.medusa_pages_served(p, None, FAKE, 5, FAKE, None) == -1
+    assert L.medusa_pages_served(p, FAKE, FAKE, -1, FAKE, None) == -1
+    assert L.medusa_pages_served(p, FAKE, None, 2, FAKE, None) == -1
+    assert L.medusa_pages_served(p, FAKE, FAKE, 2, None, None) == -1
+    assert L.medusa_pages_served(p, None, None, 0, None, None) == 0
     assert L.medusa_pages_commit(p, None, FAKE, 0, 5, None, None) == -1
     assert L.medusa_pages_commit(p, FAKE, FAKE, -1, 2, None, None) == -1
     assert L.medusa_pages_commit(p, FAKE, None, 0, 2, None, None) == -1
@@ -143,6 +148,13 @@ def test_binding_refuses_tensors_that_do_not_fit(M):
         M.medusa_paged_attn(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], **(args | {"out": torch.zeros(3, 2, 64)}))
     with pytest.raises(ValueError, match="the cache has"):
         M.medusa_paged_attn(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], **(args | {"k_pages": k[:6], "v_pages": k[:6]}))
+
+
+def test_step_refuses_an_unknown_cache():
+    from medusa_tree_speculative_gb300 import step, workloads
+
+    with pytest.raises(ValueError):
+        step.VerifyStep(workloads.get("tiny_fp32"), {}, None, 1, cache="slabs")
 
 
 def test_book_keeps_its_invariants():
