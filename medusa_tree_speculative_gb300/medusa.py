@@ -537,7 +537,7 @@ class _Torch:
         import torch
 
         cls.bf16, cls.f32 = torch.bfloat16, torch.float32
-        cls.current_device = staticmethod(torch.cuda.current_device)
+        cls.current_device = staticmethod(getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
         cls.raw_stream = staticmethod(getattr(torch._C, "_cuda_getCurrentRawStream", None) or
                                       (lambda index: torch.cuda.current_stream(index).cuda_stream))
         cls.int32 = torch.int32
@@ -567,6 +567,11 @@ def _on(t, name, index, n=None, dtype=None):
 
 
 def _ints(t, name, index, n=None):
+    """Pointer of a dense int32 tensor; a call has up to six, so what fits takes one step."""
+    if t is None:
+        return None
+    if t.dtype is _Torch.int32 and t.get_device() == index and t.is_contiguous() and (n is None or t.numel() == n):
+        return t.data_ptr()
     if _Torch.int32 is None:
         _Torch.load()
     return _on(t, name, index, n, _Torch.int32)
