@@ -36,8 +36,8 @@
  *     size returned by the matching *_workspace_size query, 256-byte aligned.
  *     Its contents are not preserved.  Calls whose kernels hand out work or
  *     elect a last CTA through counters kept in it (medusa_accept,
- *     medusa_heads_topk, medusa_heads_logits_topk) need it zero-filled before
- *     the first call and leave it ready for the next call of the same entry
+ *     medusa_heads_topk, medusa_heads_logits_topk, medusa_paged_attn) need it
+ *     zero-filled before the first call and leave it ready for the next call of the same entry
  *     point; the others need no initialisation.
  *   - Device-side data errors (a token or node index out of range, a prefix
  *     that overflows its sequence's capacity) cannot be seen by the host
@@ -604,8 +604,8 @@ int medusa_standin_embed(const int32_t* tokens, int rows, const void* emb,
  *
  * A decode step of a batch:
  *   medusa_pages_reserve   room for each row's new tokens; its list of copies
- *   medusa_pages_served    the batch without the rows that got none
  *   medusa_pages_copy      ... carried out, once per layer
+ *   medusa_pages_served    the batch without the rows that got no room
  *   medusa_paged_attn      once per layer: append, attend
  *   medusa_paged_compact   once per layer, after a tree: the accepted path
  *   medusa_pages_commit    the rows' new lengths
