@@ -174,14 +174,14 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_c
 // its maximum and sum are four shuffles.  Key rows are padded by 16 bytes
 // (eight threads' 16-byte loads of eight rows then hit different banks).  The
 // value tile loads while S is computed and the next key tile while O is.
-// Bound by shared memory: a warp's sixteen products of four rows and four keys
-// need eight 16-byte loads, which take about as many cycles as 1.5 times the
-// products (the FMA pipe is 41% busy).  345 tokens in five sequences, 16 heads
-// of 64 (four per key head), prefixes up to 2000: 74 us with the rotation's
-// launch.  Blocks of at most 16 rows have a form of their own where the call
-// has no others: one token at a prefix of 1024, 32 heads of 128, 22.6 us against
-// 28.7 in the form for 64 rows; 64 tokens, 16 heads of 128 (four per key head),
-// prefixes up to 4000, 144 against 160.
+// Bound by shared memory and by the barriers between a tile's four phases: the
+// FMA pipe is 41% busy (4 x 8 and 8 x 8 products per thread need fewer loads but
+// leave fewer warps, and gain nothing; nor do two FMAs per instruction).  345
+// tokens in five sequences, 16 heads of 64 (four per key head), prefixes up to
+// 2000: 74 us with the rotation's launch.  Blocks of at most 16 rows have a form
+// of their own where the call has no others: one token at a prefix of 1024, 32
+// heads of 128, 22.6 us against 28.7 in the form for 64 rows; 64 tokens, 16
+// heads of 128 (four per key head), prefixes up to 4000, 144 against 160.
 constexpr int kGenThreads = 256, kGenCtas = 2;  // CTAs per SM (the two cases above: 74 and 144 us; with 3: 89, 186)
 
 template <int DH, int RB, int KT>
