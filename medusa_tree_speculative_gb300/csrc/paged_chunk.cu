@@ -31,8 +31,8 @@
 // QK(j+1) may overwrite the columns from which PV(j), issued before it, reads
 // P.
 // Measured, with the launch before it: 8192 tokens of 32 heads of 128 (8 key
-// heads) 393 us, the kernel itself 363 us or 1.51 PFLOP/s, the tensor cores
-// busy for 66% of its cycles; trees of 65 rows on four prefixes up to 8192, 52
+// heads) 389 us, the kernel itself 359 us or 1.53 PFLOP/s, the tensor cores
+// busy for two thirds of its cycles; trees of 65 rows on four prefixes up to 8192, 52
 // heads of 128, 99 us at 4.8 TB/s (bound by memory: the loop over tiles runs at
 // 6.5 TB/s); eleven sequences of 1 .. 700 tokens, 40 heads of 64 (8 key heads),
 // prefixes up to 5000, 77 us (bound by the way from one tile's scores to the
@@ -578,9 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[128];
           tmem_ld32(tS, v);
           tmem_ld32(tS + 32, v + 32);
-          tmem_ld_wait();
           tmem_ld32(tS + 64, v + 64);
           tmem_ld32(tS + 96, v + 96);
+          tmem_ld_wait();
           auto mask = [&](int c0) {  // keys c0 .. c0 + 63 of the tile
             if (a.T == 0) {
               const int d = L + tok + 1 - key0;  // keys below this are seen
@@ -618,7 +618,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           mask(0);
           maxima(0);
-          tmem_ld_wait();
           mask(64);
           maxima(64);
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
