@@ -31,7 +31,7 @@
 // QK(j+1) may overwrite the columns from which PV(j), issued before it, reads
 // P.
 // Measured, with the launch before it: 8192 tokens of 32 heads of 128 (8 key
-// heads) 389 us, the kernel itself 359 us or 1.53 PFLOP/s, the tensor cores
+// heads) 389 us, the kernel itself 361 us or 1.52 PFLOP/s, the tensor cores
 // busy for two thirds of its cycles; trees of 65 rows on four prefixes up to 8192, 52
 // heads of 128, 99 us at 4.8 TB/s (bound by memory: the loop over tiles runs at
 // 6.5 TB/s); eleven sequences of 1 .. 700 tokens, 40 heads of 64 (8 key heads),
