@@ -10,9 +10,10 @@
 //     lane per (page, pool), both 64-column halves of a line in one copy, and
 //     runs on over the segments of the CTA's list;
 //   * the query warp rotates the next segment's query rows while the present
-//     one runs (two buffers).  Queries are kept as two bf16 parts, high and
-//     low, and multiplied in two MMAs: the tensor cores have time to spare
-//     here, and the scores are then as exact as the cache's keys;
+//     one runs (two buffers).  Queries and the weights P are kept as two bf16
+//     parts, high and low (2^-16 relative together), and multiplied in two
+//     MMAs: the tensor cores have time to spare here, and the result is off by
+//     its own rounding only;
 //   * warps 0-3 take 16 keys of each tile each: S = Q K^T and O += P V by
 //     mma.sync (M = 16), the running maximum and sum per warp, no barrier among
 //     them until the segment ends and their four results are joined.
@@ -27,8 +28,6 @@
 // Measured: 64 tokens with prefixes of 500 .. 8192, 32 heads of 128 on 8 key
 // heads, 184 us, 5.96 TB/s (171 with pages of 32 tokens or more: half as
 // many copies).
-// P, unlike the queries, is rounded once to bf16 (a relative 2^-8 a weight,
-// independent from key to key).
 #include "cluster.cuh"
 #include "paged_attn.cuh"
 #include "sm100.cuh"
@@ -355,8 +354,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           l0 += (z[0][0] + z[0][1]) + (z[1][0] + z[1][1]);
           l1 += (z[0][2] + z[0][3]) + (z[1][2] + z[1][3]);
-          const uint32_t p[4] = {pack2_bf16(z[0][0], z[0][1]), pack2_bf16(z[0][2], z[0][3]),
-                                 pack2_bf16(z[1][0], z[1][1]), pack2_bf16(z[1][2], z[1][3])};
+          uint32_t ph[4], pl[4];  // the weights' two parts
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float u = z[e >> 1][(e & 1) * 2], w = z[e >> 1][(e & 1) * 2 + 1];
+            ph[e] = pack2_bf16(u, w);
+            pl[e] = pack2_bf16(u - __uint_as_float(ph[e] << 16), w - __uint_as_float(ph[e] & 0xffff0000u));
+          }
           // value rows past the sequence hold whatever the page does: zeros
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
           if (edge) {
@@ -376,8 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               b[2] &= keep0;
               b[3] &= keep1;
             }
-            mma_bf16_16816(o[2 * j], p, b[0], b[1]);
-            mma_bf16_16816(o[2 * j + 1], p, b[2], b[3]);
+            mma_bf16_16816(o[2 * j], ph, b[0], b[1]);
+            mma_bf16_16816(o[2 * j + 1], ph, b[2], b[3]);
+            mma_bf16_16816(o[2 * j], pl, b[0], b[1]);
+            mma_bf16_16816(o[2 * j + 1], pl, b[2], b[3]);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[st]);
