@@ -13,7 +13,8 @@ namespace {
 // A CTA per TOK tokens and group of heads: cos and sin of a token's position
 // once per pair, in shared memory, then eight pairs per thread and step, the
 // loads of kPrepSteps steps in flight.  Queries go to q_rot with the softmax
-// scale in them, keys and values to their pages.  Every element is read and
+// scale in them (bf16: rounded, and in a second plane what the rounding left,
+// rounded), keys and values to their pages.  Every element is read and
 // written once: bound by memory for long chunks (16 tokens per CTA, all heads:
 // 8192 tokens of 48 heads, 201 MB, in 37 us), by the latency of a thread's few steps
 // for short ones (4 tokens, as many groups of heads as give a thread
@@ -157,6 +158,18 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_c
         }
         store8(reinterpret_cast<T*>(lo[u]), x);
         store8(reinterpret_cast<T*>(hi[u]), y);
+        if (sizeof(T) == 2 && h < a.H) {  // what the rounding left
+          float rx[8], ry[8];
+          load8(reinterpret_cast<const T*>(lo[u]), rx);
+          load8(reinterpret_cast<const T*>(hi[u]), ry);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            rx[j] = x[j] - rx[j];
+            ry[j] = y[j] - ry[j];
+          }
+          store8(dst[u] + a.q_low + c * 8, rx);
+          store8(dst[u] + a.q_low + DH / 2 + c * 8, ry);
+        }
       }
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
@@ -460,7 +473,7 @@ PagedWorkspace workspace_of(int total_q, int H, int Dh, medusa_dtype dtype, int 
   PagedWorkspace w;
   const bool bf16 = dtype == MEDUSA_BF16;
   w.q_rot = kCounterBytes;
-  w.part = align_up(w.q_rot + (size_t)total_q * H * Dh * (bf16 ? 2 : 4), 256);
+  w.part = align_up(w.q_rot + (size_t)total_q * H * Dh * 4, 256);  // float32, or two bf16 parts
   const size_t few = bf16 ? paged_decode_part_bytes(Dh, sms) : generic_part_bytes(16, Dh, sms);
   const size_t many = bf16 ? paged_chunk_part_bytes(Dh, sms) : generic_part_bytes(64, Dh, sms);
   w.total = align_up(w.part + (few > many ? few : many), 256);
@@ -609,6 +622,7 @@ extern "C" int medusa_paged_attn(const void* q, int64_t q_stride, const void* k_
   a.qscale = scale * kPagedLog2e;
   a.out = out;
   a.q_rot = ws + w.q_rot;
+  a.q_low = (int64_t)total_q * H * Dh;
   a.err = err;
   const PagedKernels k{as_stream(stream), sms};
   // One attention launch for the whole call, by its longest chunk.  A batch

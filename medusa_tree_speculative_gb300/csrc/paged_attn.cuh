@@ -53,6 +53,7 @@ struct PagedAttnArgs {
   float qscale;        // scale * log2(e)
   void* out;
   void* q_rot;         // [Hkv][total_q * g][Dh]: rotated queries times qscale
+  int64_t q_low;       // bf16: elements from q_rot to what its rounding left, rounded
   int* counters;
   float* part;         // two partials per CTA: RB rows of Dh sums, then RB (max, sum) pairs
   int32_t* err;

@@ -2,15 +2,16 @@
 // tensor cores (tcgen05, accumulators in tensor memory).
 //
 // A block of up to 256 query rows is two MMA tiles of 128 rows ("lanes" 0 and
-// 1), and a tile of 128 keys costs each lane two products,
-//   S = Q K^T  (128 x 128 x Dh)   and   O += P V  (128 x Dh x 128),
-// 1024 cycles of the SM's tensor core together at Dh = 128.  While one lane's
+// 1), and a tile of KT keys (96, or 128 where heads have 64 columns) costs each
+// lane
+//   S = Q K^T  (128 x KT x Dh, twice)   and   O += P V  (128 x Dh x KT),
+// 1152 cycles of the SM's tensor core together at Dh = 128.  While one lane's
 // scores are exponentiated, the tensor core works for the other: the issuing
 // thread's order is PV0(j), QK0(j+1), PV1(j), QK1(j+1), ..., so a lane's
-// softmax has the other lane's two products, 1024 cycles, to hide behind.  The
+// softmax has the other lane's products, 1152 cycles, to hide behind.  The
 // kernel is bound by the tensor core where that holds.
 //   * warps 0-3 and 4-7 are the lanes' softmax: a thread per query row (its
-//     tensor-memory lane) reads 128 scores and writes P = 2^(S - m) in bf16
+//     tensor-memory lane) reads KT scores and writes P = 2^(S - m) in bf16
 //     over them in tensor memory, with no exchange between threads.  (Two
 //     threads per row, which agree on the maximum through shared memory, take
 //     less time from scores to P, but issue 1.7 times the instructions, and the
@@ -24,19 +25,27 @@
 // tiles in turn, with the same queries, and their results are joined at the
 // segment's end.
 // Queries come rotated and scaled from the launch before this one, which also
-// appends the chunk; P is rounded to bf16, as the queries are (2^-8 relative
-// each, independent from element to element): the MMA takes both factors in
-// one type, and the values are bf16.
+// appends the chunk, as two bf16 parts, high and low, 2^-16 relative together:
+// an error of a query is one of every score, and grows with the scores.  Each
+// part has a product of its own.  (One part alone takes 361 us in place of 520
+// for 8192 tokens of heads of 128, and its error, at scores of deviation 1, is
+// as large as the result's own rounding.)  The low parts take the room that tiles of
+// 128 keys would need at Dh = 128.
+// P is rounded once to bf16 where a call has two query tiles: a relative 2^-8 a
+// weight at most, independent from key to key, so no larger in the result than
+// its own rounding, whatever the scores.  (In two parts: 100 us in place of 79
+// for the mixed batch below, 540 in place of 361 for the prompt, both with queries
+// in one.)  A call with one query tile, bound by memory, has time for two
+// parts of P as well (4 of its 110 us).
 // MMAs that one thread issues run in issue order on the CTA's tensor core:
 // QK(j+1) may overwrite the columns from which PV(j), issued before it, reads
 // P.
 // Measured, with the launch before it: 8192 tokens of 32 heads of 128 (8 key
-// heads) 389 us, the kernel itself 361 us or 1.52 PFLOP/s, the tensor cores
-// busy for two thirds of its cycles; trees of 65 rows on four prefixes up to 8192, 52
-// heads of 128, 99 us at 4.8 TB/s (bound by memory: the loop over tiles runs at
-// 6.5 TB/s); eleven sequences of 1 .. 700 tokens, 40 heads of 64 (8 key heads),
-// prefixes up to 5000, 77 us (bound by the way from one tile's scores to the
-// next one's).
+// heads) 564 us, 1.46 PFLOP/s with both parts' products; trees of 65 rows on
+// four prefixes up to 8192, 52 heads of 128, 110 us (bound by memory in the
+// loop over tiles; plan, first loads and joins around it); eleven sequences of
+// 1 .. 700 tokens, 40 heads of 64 (8 key heads), prefixes up to 5000, 88 us
+// (bound by the way from one tile's scores to the next one's).
 #include <utility>
 
 #include "paged_attn.cuh"
@@ -47,9 +56,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr int RB = 256, KT = 128;
+constexpr int RB = 256;
 // places that beginning and ending a unit is worth
-constexpr int kCost = 2;  // 8192 tokens: 433, 406, 407 us at 1, 2, 3; a batch of trees: 101, 103, 101
+constexpr int kCost = 2;  // 8192 tokens: 585, 565, 565 us at 1, 2, 3; the mixed batch 89, 88, 90; trees 111, 110, 111
 constexpr int kThreads = 384;  // two softmax groups of 128; the load warp, the MMA warp and two segment warps
 constexpr int kSoft = 256, kLoadWarp = 8, kMmaWarp = 9;
 // Registers: the block starts with 168 a thread (384 x 168 = 64512); the softmax
@@ -60,22 +69,29 @@ static_assert(kSoft * kSoftRegs + (kThreads - kSoft) * kOtherRegs <= kThreads * 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSmemBase = 1024;  // where dynamic shared memory starts in a kernel without static; checked
 
+// Keys that one copy may bring: a tile is a whole number of copies, and they
+// begin where a page's lines may (a page ends inside none of them).
+MDEV __host__ constexpr int key_box(int kt) { return kt & -kt; }
+
 template <uint32_t B>
 struct Half {
   static constexpr uint32_t value = B;
 };
 
 // NARROW: a call whose chunks all have one query tile (at most 128 rows per key
-// head), bound by memory: the second tile's place goes to the ring (trees of 65
-// rows on four prefixes up to 8192: 99.8 us, 102.6 without).
+// head), bound by memory: the second tile's place goes to the ring.
 template <int DH, bool NARROW>
 struct Cfg {
   static constexpr int kHalves = DH / 64;
-  static constexpr uint32_t kHalf = 128 * 128;          // 128 rows of one swizzle span
-  static constexpr uint32_t kTile = kHalf * kHalves;    // 128 rows x DH bf16
+  // keys per tile: as many as leave room for both parts of the queries
+  static constexpr int KT = DH == 64 ? 128 : 96;
+  static constexpr uint32_t kQHalf = 128 * 128;           // 128 rows of one swizzle span
+  static constexpr uint32_t kQTile = kQHalf * kHalves;    // 128 rows x DH bf16
+  static constexpr int kQTiles = NARROW ? 1 : 2;          // their high parts, then their low parts
+  static constexpr uint32_t kHalf = KT * 128, kTile = kHalf * kHalves;  // KT keys, or values
   // a stage: the values of a tile and the keys of the next, one wait for both
   static constexpr int kStages = !NARROW ? 2 : DH == 128 ? 3 : 6;
-  static constexpr uint32_t kRingOff = (NARROW ? 1 : 2) * kTile;
+  static constexpr uint32_t kRingOff = 2 * kQTiles * kQTile;
   static constexpr uint32_t kBarOff = kRingOff + kStages * 2 * kTile;
   static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 1 + 1 + 1;
   static constexpr uint32_t kSegOff = (kBarOff + kBars * 8 + 16 + 15) & ~15u;    // [2 lanes][2] segments
@@ -176,14 +192,17 @@ template <int DH>
 struct Products {
   using G = Cfg<DH, false>;
   static constexpr uint64_t kHi = (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32;
+  static constexpr int KT = G::KT;
+  static constexpr uint32_t kQHalf16 = G::kQHalf >> 4, kQTile16 = G::kQTile >> 4;
   static constexpr uint32_t kHalf16 = G::kHalf >> 4, kTile16 = G::kTile >> 4;
   static constexpr uint32_t kQ = kSmemBase >> 4 | 1u << 16, kK = (kSmemBase + G::kRingOff) >> 4 | 1u << 16;
   static constexpr uint32_t kV = ((kSmemBase + G::kRingOff) >> 4) + kTile16 | kHalf16 << 16;
-  static __host__ __device__ constexpr uint32_t step(int kk) { return (kk >> 2) * kHalf16 + (kk & 3) * 2; }
-  template <uint32_t I, uint32_t QT, uint32_t B, int... KK>
+  static __host__ __device__ constexpr uint32_t step(int kk, uint32_t half) { return (kk >> 2) * half + (kk & 3) * 2; }
+  // step KK of the high parts (PART 0) or the low parts (1) of query tile QT
+  template <uint32_t I, uint32_t QT, uint32_t B, int PART, int... KK>
   static MDEV void qk_steps(std::integer_sequence<int, KK...>) {
-    (umma_const<I * 128, kHi | (kQ + QT * kTile16 + step(KK)), kHi | (kK + B * 2 * kTile16 + step(KK)),
-                idesc_bf16_f32(128, KT), KK != 0>(),
+    (umma_const<I * 128, kHi | (kQ + (PART * G::kQTiles + QT) * kQTile16 + step(KK, kQHalf16)),
+                kHi | (kK + B * 2 * kTile16 + step(KK, kHalf16)), idesc_bf16_f32(128, KT), PART != 0 || KK != 0>(),
      ...);
   }
   template <uint32_t I, uint32_t B, int... J>
@@ -195,7 +214,8 @@ struct Products {
   }
   template <uint32_t I, uint32_t QT, uint32_t B>
   static MDEV void qk() {
-    qk_steps<I, QT, B>(std::make_integer_sequence<int, DH / 16>());
+    qk_steps<I, QT, B, 0>(std::make_integer_sequence<int, DH / 16>());
+    qk_steps<I, QT, B, 1>(std::make_integer_sequence<int, DH / 16>());
   }
   template <uint32_t I, uint32_t B>
   static MDEV void pv(uint32_t add) {
@@ -229,9 +249,11 @@ MDEV void wait_at(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
 
 template <int DH, bool NARROW>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedAttnArgs a) {
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQl,
+                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ PagedAttnArgs a) {
   using G = Cfg<DH, NARROW>;
+  constexpr int KT = G::KT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase != kSmemBase) {
@@ -270,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
     *s_abort = 0;
     tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmQl);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
@@ -294,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------ keys and values
       // the appended tokens, written by the launch before
       asm volatile("griddepcontrol.wait;\n\tfence.proxy.async.global;\n" ::: "memory");
-      const int box = min(a.p.page_size, KT), runs = KT / box;
+      const int box = min(a.p.page_size, key_box(KT)), runs = KT / box;
       const int op_run = lane / G::kHalves, op_half = lane % G::kHalves;
       const bool mine = op_run < runs;
       const int nowhere = (a.p.num_pages * a.Hkv) << a.p.shift;  // past the pool: reads zeros
@@ -337,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&full[j % G::kStages], (uint32_t)(j / G::kStages) & 1u)) *abort_flag = 1;
     } else if (warp == kMmaWarp && any) {
       // ------------------------------------------------ MMAs
-      // One thread issues 32 products' instructions per tile of 2048 cycles.
+      // One thread issues 44 products' instructions per tile of 2304 cycles.
       // Issuing does not run ahead of the tensor core by more than an
       // instruction or two, and beside the softmax warps a wait costs 150
       // cycles even where it is over: so addresses are constants, and there are
@@ -351,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // j & 1 has tile j; QK runs two tiles ahead of PV, of the segment only.
         if (elect_one()) {
           constexpr uint32_t kStage16 = 2 * G::kTile >> 4, kHalf16 = G::kHalf >> 4, kTile16 = G::kTile >> 4;
+          constexpr uint32_t kQHalf16 = G::kQHalf >> 4, kQTile16 = G::kQTile >> 4;
           constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
           constexpr uint32_t q16 = kSmemBase >> 4 | 1u << 16, k16 = (kSmemBase + G::kRingOff) >> 4 | 1u << 16;
           constexpr uint32_t v16 = ((kSmemBase + G::kRingOff) >> 4) + kTile16 | kHalf16 << 16;
@@ -369,10 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_at(bars + kst * 8, kph, abort_flag);
             tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk)
-              umma_words(i * 128, q16 + (kk >> 2) * kHalf16 + (kk & 3) * 2,
+            for (int e = 0; e < 2 * DH / 16; ++e) {  // the queries' high parts, then their low parts
+              const int kk = e % (DH / 16), part = e / (DH / 16);
+              umma_words(i * 128, q16 + part * kQTile16 + (kk >> 2) * kQHalf16 + (kk & 3) * 2,
                          k16 + kst * kStage16 + (kk >> 2) * kHalf16 + (kk & 3) * 2, kDescHi, idesc_bf16_f32(128, KT),
-                         kk != 0);
+                         e != 0);
+            }
             commit_at(kS + i * 8);
             commit_at(kEmpty + kst * 8);
             if (first) commit_at(kEmpty + kst * 8);  // the first stage has no values
@@ -393,9 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               pph[i] ^= 1u;
               tc_fence_after();
 #pragma unroll
-              for (int k = 0; k < KT / 16; ++k)
-                umma_ts_words(256 + i * 128, i * 128 + k * 8, v16 + vst * kStage16 + k * (2048 >> 4), kDescHi,
-                              idesc_bf16_f32(128, DH) | 1u << 16, k == 0 ? (uint32_t)(j > 1) : 1u);
+              for (int k = 0; k < 2 * KT / 16; ++k)  // P's high parts, then its low parts
+                umma_ts_words(256 + i * 128, i * 128 + k * 8, v16 + vst * kStage16 + k % (KT / 16) * (2048 >> 4),
+                              kDescHi, idesc_bf16_f32(128, DH) | 1u << 16, k == 0 ? (uint32_t)(j > 1) : 1u);
               commit_at(kEmpty + vst * 8);
               next_stage(vst, vph);
               if (j + 2 < n) {
@@ -536,10 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             const int tiles = min(tb, sg.s.n - sg.u * tb) * a.g > 128 ? 2 : 1;
             const int y = (sg.head * a.total_q + sg.s.q0 + sg.u * tb) * a.g;
-            mbar_expect_tx(q_full, tiles * G::kTile);
+            mbar_expect_tx(q_full, 2 * tiles * G::kQTile);
             for (int k = 0; k < tiles; ++k)
-              for (int h = 0; h < G::kHalves; ++h)
-                tma_load_2d(smem + k * G::kTile + h * G::kHalf, &tmQ, q_full, h * 64, y + k * 128);
+              for (int h = 0; h < G::kHalves; ++h) {
+                tma_load_2d(smem + k * G::kQTile + h * G::kQHalf, &tmQ, q_full, h * 64, y + k * 128);
+                tma_load_2d(smem + (G::kQTiles + k) * G::kQTile + h * G::kQHalf, &tmQl, q_full, h * 64, y + k * 128);
+              }
           }
         }
         __syncwarp();
@@ -575,23 +603,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           paged_wait(&s_full[i], cnt & 1u, abort_flag);
           __syncwarp();
           tc_fence_after();
-          uint32_t v[128];
-          tmem_ld32(tS, v);
-          tmem_ld32(tS + 32, v + 32);
-          tmem_ld32(tS + 64, v + 64);
-          tmem_ld32(tS + 96, v + 96);
+          uint32_t v[KT];
+#pragma unroll
+          for (int c = 0; c < KT; c += 32) tmem_ld32(tS + c, v + c);
           tmem_ld_wait();
-          auto mask = [&](int c0) {  // keys c0 .. c0 + 63 of the tile
+          constexpr int kPiece = KT % 64 ? KT : 64;
+          auto mask = [&](int c0) {  // keys c0 .. c0 + kPiece - 1 of the tile
             if (a.T == 0) {
               const int d = L + tok + 1 - key0;  // keys below this are seen
-              if (__any_sync(0xffffffffu, d < c0 + 64)) {
+              if (__any_sync(0xffffffffu, d < c0 + kPiece)) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e) v[c0 + e] = c0 + e < d ? v[c0 + e] : 0xff800000u;
+                for (int e = 0; e < kPiece; ++e) v[c0 + e] = c0 + e < d ? v[c0 + e] : 0xff800000u;
               }
-            } else if (key0 + c0 + 64 > L) {
+            } else if (key0 + c0 + kPiece > L) {
               const uint32_t* anc = a.anc + (int64_t)tok * a.W;
 #pragma unroll
-              for (int w = 0; w < 2; ++w) {
+              for (int w = 0; w < kPiece / 32; ++w) {
                 const int j0 = key0 + c0 + 32 * w, n0 = j0 - L;  // tree node of bit 0 (negative: prefix keys first)
                 uint32_t bits = 0xffffffffu;
                 if (n0 >= 0) {
@@ -611,15 +638,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           auto maxima = [&](int c0) {
 #pragma unroll
-            for (int e = 0; e < 64; e += 8)
+            for (int e = 0; e < kPiece; e += 8)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(v[c0 + e + 2 * k])), __uint_as_float(v[c0 + e + 2 * k + 1]));
           };
-          mask(0);
-          maxima(0);
-          mask(64);
-          maxima(64);
+#pragma unroll
+          for (int c = 0; c < KT; c += kPiece) {
+            mask(c);
+            maxima(c);
+          }
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           const bool far = mt > m + 8.f;
           if (__any_sync(0xffffffffu, far)) {  // a segment's first tile, and seldom after
@@ -644,8 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float base = m == -INFINITY ? 0.f : m;
           float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t p[16];
+          for (int h = 0; h < KT / 32; ++h) {
+            uint32_t p[16], low[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float u = __uint_as_float(v[32 * h + 2 * e]), w = __uint_as_float(v[32 * h + 2 * e + 1]);
@@ -654,8 +682,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               w = ex2(w);
               add2(sa[e & 1], sb[e & 1], u, w);
               p[e] = pack2_bf16(u, w);
+              if (NARROW) low[e] = pack2_bf16(u - __uint_as_float(p[e] << 16), w - __uint_as_float(p[e] & 0xffff0000u));
             }
             tmem_st_32x32b_x16(tS + h * 16, p);
+            if (NARROW) tmem_st_32x32b_x16(tS + KT / 2 + h * 16, low);
           }
           l += (sa[0] + sb[0]) + (sa[1] + sb[1]);
           tmem_st_wait();
@@ -664,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (key_base + (j + 1) * KT > nkeys && (i == 0 || !wide)) {
             const int n = it + j + 1, st = n % G::kStages;  // the values' fill and stage
             paged_wait(&full[st], (uint32_t)(n / G::kStages) & 1u, abort_flag);
-            if (key_base + j * KT + r >= nkeys) {
+            if (r < KT && key_base + j * KT + r >= nkeys) {
 #pragma unroll
               for (int c = 0; c < G::kHalves * 8; ++c)
                 *reinterpret_cast<uint4*>(smem + G::kRingOff + st * 2 * G::kTile + G::kTile + (c >> 3) * G::kHalf +
@@ -821,17 +851,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int DH, bool NARROW>
 int run(const PagedAttnArgs& a, const PagedKernels& k) {
-  CUtensorMap tmQ, tmK, tmV;
-  const int box = a.p.page_size < KT ? a.p.page_size : KT;
-  if (!make_rows_map(&tmQ, a.q_rot, (int64_t)a.total_q * a.H, DH, 128) ||
-      !make_pool_map(&tmK, a.k_pages, a, DH, box) || !make_pool_map(&tmV, a.v_pages, a, DH, box))
+  CUtensorMap tmQ, tmQl, tmK, tmV;
+  const int most = key_box(Cfg<DH, NARROW>::KT), box = a.p.page_size < most ? a.p.page_size : most;
+  const int64_t rows = (int64_t)a.total_q * a.H;
+  if (!make_rows_map(&tmQ, a.q_rot, rows, DH, 128) ||
+      !make_rows_map(&tmQl, static_cast<uint16_t*>(a.q_rot) + a.q_low, rows, DH, 128) || !make_pool_map(&tmK, a.k_pages, a, DH, box) || !make_pool_map(&tmV, a.v_pages, a, DH, box))
     return fail(MEDUSA_ERR_CUDA, "medusa_paged_attn: cuTensorMapEncodeTiled failed");
   auto* fn = paged_chunk_kernel<DH, NARROW>;
   static std::atomic<uint64_t> done{0};
   // the registers' redistribution would wait for ever if the block had fewer to give
   if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), Cfg<DH, NARROW>::smem, kLaunchRegs, &done, "medusa_paged_attn"))
     return rc;
-  launch_after(fn, dim3(k.sms), dim3(kThreads), Cfg<DH, NARROW>::smem, k.stream, tmQ, tmK, tmV, a);
+  launch_after(fn, dim3(k.sms), dim3(kThreads), Cfg<DH, NARROW>::smem, k.stream, tmQ, tmQl, tmK, tmV, a);
   return check_launch("medusa_paged_attn");
 }
 

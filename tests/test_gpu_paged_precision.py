@@ -1,12 +1,14 @@
 """How exact the chunk attention over the paged cache is: the 2-norm of its error against 64-bit formulas, relative to
 the result's.  A bound on every element for itself has to allow for the worst case of thousands of roundings that in
 truth average out; these ones have no such slack."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 from paged_util import rotate
-from test_gpu_paged import Chunk
+from test_gpu_paged import Chunk, cartesian_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -62,10 +64,13 @@ def off(c, want):
 
 
 def bound(c, r):
-    """Queries and weights have two bf16 parts (2^-16 together) and sums 32 bits (scores up to some ten, so weights to 2^-19): the
+    """Queries have two bf16 parts (2^-16 together) and sums 32 bits (scores up to some ten, so weights to 2^-19): the
     result is off by its own rounding, r, up to the chance of another sample (under 2% for thousands of elements), and
-    by less than 2^-14 besides."""
-    return 1.05 * r + 2.0 ** -14
+    by less than 2^-14 besides.  Chunks of more than 128 rows per key head round the weights once to bf16 as well: a
+    rounding is uniform over a step, 2^-8 / sqrt(3) in units of the binade's lower end, and mantissas spread evenly over
+    their logarithm are sqrt(3 / (2 ln 2)) such units in the mean square: 0.00153 of the weight, independent of r."""
+    w = 0.00153 if max(c.n) * (c.H // c.Hkv) > 128 else 0.0
+    return 1.05 * math.hypot(r, w) + 2.0 ** -14
 
 
 @pytest.mark.parametrize("H,Hkv,Dh,ps,n,L", [
@@ -75,6 +80,31 @@ def bound(c, r):
 def test_few_rows(M, H, Hkv, Dh, ps, n, L):
     c = Chunk(M, "bf16", H, Hkv, Dh, ps, n, L, seed=31)
     c.run()  # the appended keys, which `exact` reads
+    e, r = off(c, exact(c))
+    print(e, r)
+    assert e <= bound(c, r)
+
+
+CHUNKS = [  # H, Hkv, Dh, ps, n, L
+    (4, 1, 128, 16, [64, 5], [0, 4000]), (8, 8, 64, 32, [70, 128], [3000, 900]), (2, 2, 128, 64, [129, 500], [2000, 40]),
+    (10, 2, 64, 32, [300, 1, 41], [100, 5000, 700]), (4, 4, 128, 128, [1500], [0])]
+
+
+@pytest.mark.parametrize("H,Hkv,Dh,ps,n,L", CHUNKS)
+def test_chunks(M, H, Hkv, Dh, ps, n, L):
+    c = Chunk(M, "bf16", H, Hkv, Dh, ps, n, L, seed=32)
+    c.run()
+    e, r = off(c, exact(c))
+    print(e, r)
+    assert e <= bound(c, r)
+
+
+@pytest.mark.parametrize("s,nodes,H,Hkv,Dh", [((4, 4, 4), 64, 6, 6, 128), ((4, 4, 4), 84, 8, 4, 64),
+                                             ((2, 2, 2), 14, 40, 4, 128), ((4, 4, 4, 4), 340, 2, 2, 128)])
+def test_trees(M, s, nodes, H, Hkv, Dh):
+    t = cartesian_tree(M, list(s), nodes)
+    c = Chunk(M, "bf16", H, Hkv, Dh, 32, [t.T, t.T], [333, 4000], tree=t, seed=nodes)
+    c.run()
     e, r = off(c, exact(c))
     print(e, r)
     assert e <= bound(c, r)
