@@ -108,3 +108,18 @@ def test_trees(M, s, nodes, H, Hkv, Dh):
     e, r = off(c, exact(c))
     print(e, r)
     assert e <= bound(c, r)
+
+
+@pytest.mark.parametrize("H,Hkv,Dh,ps,n,L", [
+    (8, 8, 64, 16, [1] * 40, [8000] * 40), (8, 8, 64, 64, [1] * 16, [30000] * 16), (16, 16, 128, 16, [1] * 20, [9000] * 20),
+    (16, 4, 64, 16, [200] * 4, [6000] * 4), (8, 8, 128, 32, [150] * 4, [5000] * 4)])
+def test_float32_long_prefixes(M, H, Hkv, Dh, ps, n, L):
+    """Units of thousands of keys per CTA.  A score's error is that of 64 or 128 products added in turn, about 11 steps
+    of 2^-25 of it, 3e-7, and every weight's as much; the sum over a tile adds 8 steps (1e-7), the sum of at most 940
+    tiles 30 (weighed by their growing partial sums half of it: 4e-7), the normaliser as much.  Their squares' sum is
+    the square of 6e-7, where a sum that runs over single keys would have 100 steps (3e-6)."""
+    c = Chunk(M, "f32", H, Hkv, Dh, ps, n, L, seed=33)
+    c.run()
+    e, _ = off(c, exact(c))
+    print(e)
+    assert e <= 1e-6
