@@ -226,8 +226,11 @@ __global__ void __launch_bounds__(kGenThreads, kGenCtas) paged_generic_kernel(co
   const int64_t total = pl.total, grid = min((int64_t)gridDim.x, total);
   const int tb = RB / a.g;
   Segment sg;
-  if (x >= x1 || !seek_segment<RB, KT, 1>(a, sc, x, x1, sg)) return;
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the rotated queries and the appended tokens
+  const bool any = x < x1 && seek_segment<RB, KT, 1>(a, sc, x, x1, sg);
+  // the rotated queries and the appended tokens; and no grid ends before the
+  // launch that it follows, whose reads the next call on the stream may change
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (!any) return;
   while (true) {
     const SeqInfo& s = sg.s;
     const int nkeys = s.L + s.n, tok0 = sg.u * tb, live = min(tb, s.n - tok0) * a.g;

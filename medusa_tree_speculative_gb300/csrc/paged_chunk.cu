@@ -311,6 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;  // 0: all of it
   const int tb = RB / a.g;
+  // A CTA without work waits here for the launch before this one: the grid must
+  // not end before that one's reads, which the next call on the stream may
+  // change.  With work, its loading warps wait.
+  if (!any) asm volatile("griddepcontrol.wait;\n" ::: "memory");
   if (warp >= kSoft / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     if (warp == kLoadWarp && any) {
