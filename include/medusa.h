@@ -91,7 +91,8 @@ enum {
   MEDUSA_DEVERR_LENGTH = 8,   /* accept_len outside [0, K] */
   MEDUSA_DEVERR_TIMEOUT = 16, /* a bounded on-chip wait gave up (internal fault) */
   MEDUSA_DEVERR_PAGE = 32,    /* a page outside the pool, or a row's state that contradicts itself */
-  MEDUSA_DEVERR_ROW = 64      /* a cache row outside its range, named twice or not empty */
+  MEDUSA_DEVERR_ROW = 64,     /* a cache row outside its range, named twice or not empty */
+  MEDUSA_DEVERR_LAYOUT = 128  /* shared memory does not begin where the kernel was built for: it did nothing */
 };
 
 typedef struct medusa_tree {

@@ -40,7 +40,8 @@ int sm_count() {
   return n;
 }
 
-int prepare_kernel(const void* kernel, size_t smem, int min_regs, std::atomic<uint64_t>* done, const char* what) {
+int prepare_kernel(const void* kernel, size_t smem, int min_regs, int smem_base, std::atomic<uint64_t>* done,
+                   const char* what) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return check_launch(what);
   const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
@@ -52,6 +53,13 @@ int prepare_kernel(const void* kernel, size_t smem, int min_regs, std::atomic<ui
   if (attr.numRegs < min_regs)
     return fail(MEDUSA_ERR_CUDA, "%s: the kernel was built with %d registers a thread, it needs %d", what, attr.numRegs,
                 min_regs);
+  int reserved = 0;  // what the system keeps comes first, then a kernel's static shared memory
+  if (smem_base > 0 &&
+      cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess)
+    return check_launch(what);
+  if (smem_base > 0 && reserved + (int)attr.sharedSizeBytes != smem_base)
+    return fail(MEDUSA_ERR_CUDA, "%s: dynamic shared memory begins at byte %d here, the kernel was built for %d", what,
+                reserved + (int)attr.sharedSizeBytes, smem_base);
   done->fetch_or(bit, std::memory_order_relaxed);
   return MEDUSA_OK;
 }

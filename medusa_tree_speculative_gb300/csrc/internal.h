@@ -76,8 +76,10 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), int cl, dim3 grid, dim3 blo
 // Opt a kernel in to `smem` bytes of shared memory, once per device (`done`: a
 // static of the caller's, a bit per device).  Returns the kernel's attributes'
 // status, MEDUSA_OK or MEDUSA_ERR_CUDA, and with min_regs > 0 checks that it
-// was built with at least that many registers a thread.
-int prepare_kernel(const void* kernel, size_t smem, int min_regs, std::atomic<uint64_t>* done, const char* what);
+// was built with at least that many registers a thread, with smem_base > 0 that
+// its dynamic shared memory begins at that byte of the block's.
+int prepare_kernel(const void* kernel, size_t smem, int min_regs, int smem_base, std::atomic<uint64_t>* done,
+                   const char* what);
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 }  // namespace medusa

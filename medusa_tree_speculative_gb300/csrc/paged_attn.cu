@@ -469,7 +469,7 @@ int run_generic(const PagedAttnArgs& a, const PagedKernels& k) {
   using G = Gen<DH, RB, KT>;
   auto* fn = paged_generic_kernel<DH, RB, KT>;
   static std::atomic<uint64_t> done{0};
-  if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), G::smem, 0, &done, "medusa_paged_attn")) return rc;
+  if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), G::smem, 0, 0, &done, "medusa_paged_attn")) return rc;
   launch_after(fn, dim3(k.sms * kGenCtas), dim3(kGenThreads), G::smem, k.stream, a);
   return check_launch("medusa_paged_attn");
 }

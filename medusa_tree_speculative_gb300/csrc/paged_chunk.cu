@@ -67,7 +67,9 @@ constexpr int kSoft = 256, kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kLaunchRegs = 168, kSoftRegs = 208, kOtherRegs = 88;
 static_assert(kSoft * kSoftRegs + (kThreads - kSoft) * kOtherRegs <= kThreads * kLaunchRegs, "registers");
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSmemBase = 1024;  // where dynamic shared memory starts in a kernel without static; checked
+// Where dynamic shared memory begins in a kernel without static: behind what the
+// system keeps of a block's.  prepare_kernel asks the device, the kernel checks.
+constexpr uint32_t kSmemBase = 1024;
 
 // Keys that one copy may bring: a tile is a whole number of copies, and they
 // begin where a page's lines may (a page ends inside none of them).
@@ -256,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int KT = G::KT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  if (sbase != kSmemBase) {
-    if (threadIdx.x == 0) set_err(a.err, MEDUSA_DEVERR_TIMEOUT);
+  if (sbase != kSmemBase) {  // the host has asked the device, too
+    if (threadIdx.x == 0) set_err(a.err, MEDUSA_DEVERR_LAYOUT);
     return;
   }
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kBarOff);  // [stages] TMA -> MMA
@@ -864,7 +866,8 @@ int run(const PagedAttnArgs& a, const PagedKernels& k) {
   auto* fn = paged_chunk_kernel<DH, NARROW>;
   static std::atomic<uint64_t> done{0};
   // the registers' redistribution would wait for ever if the block had fewer to give
-  if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), Cfg<DH, NARROW>::smem, kLaunchRegs, &done, "medusa_paged_attn"))
+  if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), Cfg<DH, NARROW>::smem, kLaunchRegs, kSmemBase, &done,
+                              "medusa_paged_attn"))
     return rc;
   launch_after(fn, dim3(k.sms), dim3(kThreads), Cfg<DH, NARROW>::smem, k.stream, tmQ, tmQl, tmK, tmV, a);
   return check_launch("medusa_paged_attn");

@@ -545,7 +545,7 @@ int run(const PagedAttnArgs& a, const PagedKernels& k) {
     return fail(MEDUSA_ERR_CUDA, "medusa_paged_attn: cuTensorMapEncodeTiled failed");
   auto* fn = paged_decode_kernel<DH, CL>;
   static std::atomic<uint64_t> done{0};
-  if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), Cfg<DH>::smem, 0, &done, "medusa_paged_attn")) return rc;
+  if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), Cfg<DH>::smem, 0, 0, &done, "medusa_paged_attn")) return rc;
   if (CL == 1) launch_kernel(fn, dim3(k.sms), dim3(kThreads), Cfg<DH>::smem, k.stream, tmK, tmV, a);
   else launch_cluster(fn, CL, dim3(a.B * a.Hkv * CL), dim3(kThreads), Cfg<DH>::smem, k.stream, tmK, tmV, a);
   return check_launch("medusa_paged_attn");

@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_PKG, "libmedusa.so")
 MEDUSA_F32, MEDUSA_BF16 = 0, 1
 MAX_T, MAX_K, MAX_S, MAX_B, MAX_ROWS = 512, 8, 16, 16, 1024
 STATUS = {0: "OK", -1: "INVALID", -2: "UNSUPPORTED", -3: "CAPACITY", -4: "WORKSPACE", -5: "CUDA"}
-DEVERR = {1: "TOKEN", 2: "NODE", 4: "CAPACITY", 8: "LENGTH", 16: "TIMEOUT", 32: "PAGE", 64: "ROW"}
+DEVERR = {1: "TOKEN", 2: "NODE", 4: "CAPACITY", 8: "LENGTH", 16: "TIMEOUT", 32: "PAGE", 64: "ROW", 128: "LAYOUT"}
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(

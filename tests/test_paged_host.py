@@ -187,3 +187,16 @@ def test_plain_attention_of_a_row_without_keys():
     assert (out[1] == 0).all() and torch.isfinite(tol).all()
     p = torch.softmax(q[0] @ k[:2].T, -1)
     assert torch.allclose(out[0], p @ v[:2])
+
+
+def test_device_errors_have_names(M):
+    """The binding names every bit of the header, each fault its own."""
+    import re
+    from pathlib import Path
+
+    text = (Path(__file__).resolve().parent.parent / "include" / "medusa.h").read_text()
+    bits = {int(v): n for n, v in re.findall(r"MEDUSA_DEVERR_(\w+) = (\d+)", text)}
+    assert bits == M.DEVERR
+    assert [n for v, n in sorted(bits.items())] == ["TOKEN", "NODE", "CAPACITY", "LENGTH", "TIMEOUT", "PAGE", "ROW",
+                                                    "LAYOUT"]
+    assert sorted(bits) == [1 << k for k in range(len(bits))]
