@@ -610,6 +610,7 @@ int medusa_standin_embed(const int32_t* tokens, int rows, const void* emb,
  *   medusa_paged_attn      once per layer: append, attend
  *   medusa_paged_compact   once per layer, after a tree: the accepted path
  *   medusa_pages_commit    the rows' new lengths
+ *   medusa_pages_advance   after a tree: its tokens to the output, the next tree
  * medusa_pages_fork starts a row that continues another one's tokens,
  * medusa_pages_free ends a row or cuts it back, medusa_pages_compact moves the
  * live pages to the front of the pool.  The paper's step has no counterpart:
@@ -673,6 +674,24 @@ int medusa_pages_reserve(const medusa_pages_t* pages, const int32_t* n_new,
 int medusa_pages_served(const medusa_pages_t* pages, const int32_t* rows,
                         const int32_t* granted, int B, int32_t* served,
                         void* stream);
+
+/* The end of a verified step for a batch of which medusa_pages_served left some
+ * sequences out: b < B with served[b] >= 0 went on, the others were skipped.
+ * One that went on: next_tokens[b] <- candidates[b], its next tree, and, where
+ * out is not NULL, its root and accepted tokens are appended to out[b] as
+ * medusa_append_tokens does (with the same errors).  A skipped one:
+ * next_tokens[b] <- tokens[b], the tree it was given, which the next step tries
+ * again; accept_len[b] <- -1; out[b] and out_len[b] stay.  tokens (may be
+ * next_tokens), candidates, next_tokens: device [B][T]; served, accept_len:
+ * device [B]; accepted_nodes: device [B][Kmax+1]; out: device [B][out_cap],
+ * out_len: device [B].  B <= MEDUSA_MAX_B.  After everything else that reads
+ * accept_len and tokens. */
+int medusa_pages_advance(const int32_t* served, const int32_t* tokens,
+                         const int32_t* candidates,
+                         const int32_t* accepted_nodes, int32_t* accept_len,
+                         int B, int T, int Kmax, int32_t* next_tokens,
+                         int32_t* out, int32_t* out_len, int out_cap,
+                         int32_t* err, void* stream);
 
 /* length[rows[b]] += n_new[b] + bias for b < B (rows, n_new: device [B]; rows
  * NULL: row b).  After a chunk bias is 0; after a verified tree n_new is

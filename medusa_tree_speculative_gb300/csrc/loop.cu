@@ -1,5 +1,6 @@
 // The decode loop's glue on the device: appending each step's tokens to the
-// output, and a stand-in for the backbone forward.
+// output (and, where some sequences of a paged cache were skipped, the next tree
+// of the others), and a stand-in for the backbone forward.
 //
 // "Medusa: Simple LLM Inference Acceleration Framework with Multiple Decoding
 // Heads", decoding-step box, step 6: the step appends the root and the
@@ -18,12 +19,9 @@
 namespace medusa {
 namespace {
 
-__global__ void __launch_bounds__(32) append_tokens_kernel(const int32_t* tokens, const int32_t* accepted_nodes,
-                                                           const int32_t* accept_len, int T, int Kmax,
-                                                           int32_t* out, int32_t* out_len, int out_cap,
-                                                           int32_t* err) {
-  const int b = blockIdx.x, lane = threadIdx.x;
-  const int n = accept_len[b];
+// Sequence b's root and accepted tokens to its output, by one warp.
+MDEV void append_tokens(int b, int lane, const int32_t* tokens, const int32_t* accepted_nodes, int n, int T, int Kmax,
+                        int32_t* out, int32_t* out_len, int out_cap, int32_t* err) {
   const int L0 = out_len[b];
   if (n < 0 || n > Kmax) {
     if (lane == 0) set_err(err, MEDUSA_DEVERR_LENGTH);
@@ -48,6 +46,32 @@ __global__ void __launch_bounds__(32) append_tokens_kernel(const int32_t* tokens
   }
   __syncwarp();
   if (lane == 0) out_len[b] = L0 + n + 1;
+}
+
+__global__ void __launch_bounds__(32) append_tokens_kernel(const int32_t* tokens, const int32_t* accepted_nodes,
+                                                           const int32_t* accept_len, int T, int Kmax,
+                                                           int32_t* out, int32_t* out_len, int out_cap,
+                                                           int32_t* err) {
+  const int b = blockIdx.x;
+  append_tokens(b, threadIdx.x, tokens, accepted_nodes, accept_len[b], T, Kmax, out, out_len, out_cap, err);
+}
+
+// One CTA per sequence: the first warp appends before any token changes (tokens
+// and next_tokens may be one buffer).
+__global__ void __launch_bounds__(128) pages_advance_kernel(const int32_t* served, const int32_t* tokens,
+                                                            const int32_t* candidates, const int32_t* accepted_nodes,
+                                                            int32_t* accept_len, int T, int Kmax, int32_t* next_tokens,
+                                                            int32_t* out, int32_t* out_len, int out_cap, int32_t* err) {
+  const int b = blockIdx.x, t = threadIdx.x;
+  const bool on = served[b] >= 0;
+  if (on && out && t < 32)
+    append_tokens(b, t, tokens, accepted_nodes, accept_len[b], T, Kmax, out, out_len, out_cap, err);
+  __syncthreads();
+  const int64_t at = (int64_t)b * T;
+  const int32_t* from = on ? candidates : tokens;
+  if (from != next_tokens)
+    for (int i = t; i < T; i += blockDim.x) next_tokens[at + i] = from[at + i];
+  if (!on && t == 0) accept_len[b] = -1;
 }
 
 // hidden[r] = emb[tokens[r]] (16-byte chunks); an out-of-range token gives a
@@ -82,6 +106,22 @@ extern "C" int medusa_append_tokens(const int32_t* tokens, const int32_t* accept
     return fail(MEDUSA_ERR_INVALID, "%s: B=%d T=%d Kmax=%d out_cap=%d", fn, B, T, Kmax, out_cap);
   launch_kernel(append_tokens_kernel, dim3(B), dim3(32), 0, as_stream(stream), tokens, accepted_nodes, accept_len,
                 T, Kmax, out, out_len, out_cap, err);
+  return check_launch(fn);
+}
+
+extern "C" int medusa_pages_advance(const int32_t* served, const int32_t* tokens, const int32_t* candidates,
+                                    const int32_t* accepted_nodes, int32_t* accept_len, int B, int T, int Kmax,
+                                    int32_t* next_tokens, int32_t* out, int32_t* out_len, int out_cap, int32_t* err,
+                                    void* stream) {
+  const char* fn = "medusa_pages_advance";
+  if (!served || !tokens || !candidates || !accepted_nodes || !accept_len || !next_tokens || (out && !out_len))
+    return fail(MEDUSA_ERR_INVALID, "%s: NULL tensor", fn);
+  if (B < 1 || B > MEDUSA_MAX_B || T < 1 || T > MEDUSA_MAX_T || Kmax < 0 || Kmax > MEDUSA_MAX_K || (out && out_cap < 1))
+    return fail(MEDUSA_ERR_INVALID, "%s: B=%d T=%d Kmax=%d out_cap=%d", fn, B, T, Kmax, out_cap);
+  if (candidates == tokens || candidates == next_tokens)
+    return fail(MEDUSA_ERR_INVALID, "%s: candidates needs a buffer of its own", fn);
+  launch_kernel(pages_advance_kernel, dim3(B), dim3(128), 0, as_stream(stream), served, tokens, candidates,
+                accepted_nodes, accept_len, T, Kmax, next_tokens, out, out_len, out_cap, err);
   return check_launch(fn);
 }
 

@@ -140,7 +140,8 @@ class DecodeLoop:
         self.out_len.zero_()
 
     def launches_per_step(self) -> int:
-        return 1 + self.st.launches_per_step + 1  # embed, the step, the append
+        append = 1 if self.st.cache == "dense" else 0  # paged, the step's last launch appends
+        return 1 + self.st.launches_per_step + append  # embed, the step, the append
 
     def step(self, stream=None, side_stream=None, heads_stream=None):
         st = self.st

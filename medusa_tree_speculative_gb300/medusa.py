@@ -88,6 +88,7 @@ _SIGS = {
     "medusa_pages_fork": (I, [PAGES, P, P, I, P, P]),
     "medusa_pages_reserve": (I, [PAGES, P, P, I, P, P, P, P]),
     "medusa_pages_served": (I, [PAGES, P, P, I, P, P]),
+    "medusa_pages_advance": (I, [P, P, P, P, P, I, I, I, P, P, P, I, P, P]),
     "medusa_pages_commit": (I, [PAGES, P, P, I, I, P, P]),
     "medusa_pages_compact_workspace_size": (SZ, [I]),
     "medusa_pages_compact": (I, [PAGES, P, I, P, P, SZ, P, P]),
@@ -630,6 +631,20 @@ def medusa_pages_served(pages: Pages, rows, granted, served, stream=None):
     d, B = pages.index, served.numel()
     _check(_lib.medusa_pages_served(pages.ref, _ints(rows, "rows", d, B), _ints(granted, "granted", d, pages.rows), B,
                                     _ints(served, "served", d), _launch_on(stream, d)), "medusa_pages_served")
+
+
+def medusa_pages_advance(served, tokens, candidates, accepted_nodes, accept_len, next_tokens, out=None, out_len=None,
+                         err=None, stream=None):
+    """The served sequences take their candidates and append root and accepted tokens to out [B][cap], out_len [B]; a
+    skipped one (served -1) keeps its tree and its output, and its accept_len becomes -1."""
+    d = served.get_device()
+    (B, T), Kp = tokens.shape, accepted_nodes.shape[1]
+    _check(_lib.medusa_pages_advance(
+        _ints(served, "served", d, B), _ints(tokens, "tokens", d), _ints(candidates, "candidates", d, B * T),
+        _ints(accepted_nodes, "accepted_nodes", d, B * Kp), _ints(accept_len, "accept_len", d, B), B, T, Kp - 1,
+        _ints(next_tokens, "next_tokens", d, B * T), _ints(out, "out", d),
+        _ints(out_len, "out_len", d, B), 0 if out is None else out.numel() // B, _ints(err, "err", d),
+        _launch_on(stream, d)), "medusa_pages_advance")
 
 
 def medusa_pages_commit(pages: Pages, rows, n_new, bias: int = 0, err=None, stream=None):

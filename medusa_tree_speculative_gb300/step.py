@@ -17,7 +17,8 @@ for the next step):
 With cache="paged" the keys and values lie in the pages of a medusa_pages_t
 instead of one slab per sequence: medusa_pages_reserve, medusa_pages_served,
 medusa_pages_copy and medusa_paged_attn take the tree attention's place,
-medusa_paged_compact and medusa_pages_commit the compaction's.
+medusa_paged_compact and medusa_pages_commit the compaction's, and
+medusa_pages_advance ends the step for the sequences that had room.
 """
 from __future__ import annotations
 
@@ -159,6 +160,7 @@ class VerifyStep:
             self.n_copies = torch.zeros(1, **i32)
             self.granted = torch.zeros(M.MAX_ROWS, **i32)
             self.served = torch.zeros(B, **i32)  # the sequences' rows, -1 for those without room
+            self.candidates = torch.zeros((B, T), **i32)  # every sequence's next tree, had it had room
             self.ws_attn = torch.zeros(M.medusa_paged_attn_workspace_size(B, B * T, T, H, self.Hkv, Dh, dt),
                                        dtype=torch.uint8, device=device)
         else:
@@ -193,9 +195,12 @@ class VerifyStep:
         With cache="paged", instead of the last five: k_pages, v_pages, pages
         (a Pages), rows (the sequences' rows [B], or None: row b) and n_new
         ([pages.rows]: T for those rows, 0 for the others).  Updates the pools
-        and the pages' state; a sequence that the pool has no room for sets
-        err and is skipped: no output, its cache and length as they were, -1
-        in `served`.
+        and the pages' state.  A sequence that the pool has no room for sets
+        err (CAPACITY, and ROW for the calls that leave it out) and is skipped:
+        -1 in `served` and `accept_len`; its cache and length, its rows of
+        `out` and its share of `append` stay as they were, and next_tokens is
+        the tree that it was given, so that a later step tries it again.  What
+        the logits, heads and acceptance hold for it does not count.
 
         One stream: tree attention, LM head, acceptance, heads, candidates,
         KV compaction.  With `side_stream`: the chain LM head -> acceptance ->
@@ -203,8 +208,8 @@ class VerifyStep:
         then the KV compaction (which needs the acceptance result) run on a
         forked branch that joins `stream` at the end.  `append` = (out,
         out_len): the step's root and accepted tokens are appended there right
-        after the acceptance (so x["tokens"] may be the buffer that
-        medusa_build_candidates refills at the end of the step)."""
+        after the acceptance, paged at the step's end (x["tokens"] may be
+        next_tokens, which the next candidates fill at the end of the step)."""
         import torch
 
         main = stream if stream is not None else torch.cuda.current_stream()
@@ -245,7 +250,7 @@ class VerifyStep:
             M.medusa_accept(self.logits, x["tokens"], self.tree, self.mode, self.temperature, self.eps,
                             self.delta, self.accept_len, self.accepted_nodes, self.next_root, self.best_node,
                             self.best_logp, self.ws_accept, self.err, main)
-        if append is not None:  # box step 6: the root and the accepted tokens to the output
+        if append is not None and self.cache == "dense":  # box step 6: the root and the accepted tokens to the output
             M.medusa_append_tokens(x["tokens"], self.accepted_nodes, self.accept_len, append[0], append[1],
                                    self.err, main)
         if side is not main:
@@ -265,21 +270,28 @@ class VerifyStep:
             attention()
         if self.attn_order != "after_heads":
             compaction()
+        # which sequences had room is known on the attention's branch only: paged,
+        # next_tokens is filled once it has joined
+        filled = self.next_tokens if self.cache == "dense" else self.candidates
         if self.heads in ("split", "joint"):
             if hs is not main and self.heads == "split":
                 main.wait_stream(hs)
             M.medusa_heads_logits_topk(self.u_all, self.T, self.best_node, self.w2, self.s_heads, self.head_logits,
                                        self.topk, self.ws_w2, self.err, main)
-            M.medusa_build_candidates(self.next_root, self.topk, self.tree, self.next_tokens, main)
+            M.medusa_build_candidates(self.next_root, self.topk, self.tree, filled, main)
         else:  # the heads' last CTA also fills the next step's candidates
             M.medusa_heads_topk_candidates(x["hidden"], self.best_node, self.w1, self.b1, self.w2, self.s_heads,
                                            self.head_logits, self.topk, self.ws_heads, self.next_root, self.tree,
-                                           self.next_tokens, self.err, main)
+                                           filled, self.err, main)
         if self.attn_order == "after_heads":  # forked after the acceptance, enqueued after the heads' launches
             attention()
             compaction()
         if side is not main:
             main.wait_stream(side)
+        if self.cache == "paged":
+            out, out_len = append if append is not None else (None, None)
+            M.medusa_pages_advance(self.served, x["tokens"], self.candidates, self.accepted_nodes, self.accept_len,
+                                   self.next_tokens, out, out_len, self.err, main)
 
     def attention(self, x: dict, stream):
         """The step's tree attention (box step 1) on `stream`."""
@@ -308,9 +320,10 @@ class VerifyStep:
         acceptance 1, compaction 1, heads 2 with the candidate fill ("fused"),
         or heads 2 ("split"; 1 "joint": W1 runs in the LM head's launch) and
         candidates 1.  Paged: reserve, served, copy, attention 2 (1 up to 16
-        query rows per key head), compaction 1, commit 1."""
+        query rows per key head), compaction 1, commit 1, advance 1 (which
+        appends the step's tokens as well)."""
         heads = {"fused": 2, "split": 3, "joint": 2}[self.heads]
         if self.cache == "paged":
             attn = 1 if self.T * (self.w["H"] // self.Hkv) <= 16 else 2
-            return 3 + attn + 1 + 1 + 2 + heads
+            return 3 + attn + 1 + 1 + 2 + 1 + heads
         return (1 if self.w["dtype"] == "bf16" else 2) + 1 + 1 + 1 + heads

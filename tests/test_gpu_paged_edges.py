@@ -44,3 +44,91 @@ def test_next_call_after_a_skipped_one(M, dt):
         assert torch.equal(p.view(bits), q.view(bits))
     c.err.zero_()
     c.go()
+
+
+@pytest.mark.parametrize("name,heads,order,side", [
+    ("tiny_fp32", "fused", "after_lm", False), ("tiny_fp32", "split", "first", True), ("tiny_bf16", "fused", "after_lm", True),
+    ("tiny_bf16", "joint", "after_accept", True), ("tiny_bf16", "fused", "after_heads", True)])
+def test_sequence_without_room_is_tried_again(M, name, heads, order, side):
+    """Three sequences of one closed loop (the step's own next tokens feed it), pages for the first one's tree alone: the
+    others keep their trees and their output.  Once the first has ended, the same step goes on with them as a dense one
+    does."""
+    from medusa_tree_speculative_gb300 import step, synth, workloads
+    from parity_util import to_dev
+
+    L, ps = 21, 16
+    w = dict(workloads.get(name), B=3, L=(L, L, L))
+    tree = M.DeviceTree(step.build_tree(w))
+    T, H, Dh = tree.T, w["H"], w["Dh"]
+    x = {k: to_dev(v) for k, v in synth.make_step(w, T, 6).items()}
+    wts = {k: (None if v is None else to_dev(v)) for k, v in synth.make_weights(w, 6).items()}
+    given = x["tokens"].clone()
+    out = [torch.full((3, 40), -5, dtype=torch.int32, device="cuda") for _ in range(2)]
+    out_len = [i32([4, 0, 9]) for _ in range(2)]
+    s = torch.cuda.Stream() if side else None
+    dense = step.VerifyStep(w, wts, tree, max_prefix=L, heads=heads)
+    dense.next_tokens.copy_(given)
+    x["prefix_len"].fill_(L)
+    torch.cuda.synchronize()
+    dense.run(dict(x, tokens=dense.next_tokens), append=(out[0], out_len[0]))
+    st = step.VerifyStep(w, wts, tree, max_prefix=L, cache="paged", heads=heads, attn_order=order)
+    st.next_tokens.copy_(given)
+    pages = M.Pages(4, 8, 5, ps)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    pools = [torch.randn(5, H, ps, Dh, generator=g, device="cuda").to(x["k_cache"].dtype) for _ in range(2)]
+    M.medusa_pages_reserve(pages, i32([L, L, 0, 0]), st.copies, st.n_copies, None, st.err)
+    M.medusa_pages_commit(pages, None, i32([L, L, 0, 0]), 0, st.err)
+    M.medusa_pages_fork(pages, i32([1]), i32([3]), st.err)
+    y = dict(x, tokens=st.next_tokens, k_pages=pools[0], v_pages=pools[1], pages=pages, rows=i32([0, 3, 1]),
+             n_new=i32([T, T, 0, T]))
+    torch.cuda.synchronize()
+    st.run(y, side_stream=s, append=(out[1], out_len[1]))
+    torch.cuda.synchronize()
+    A = dense.accept_len.tolist()
+    assert st.err.item() == CAPACITY | ROW and st.served.tolist() == [0, -1, -1]
+    assert st.accept_len.tolist() == [A[0], -1, -1]
+    assert torch.equal(st.next_tokens[1:], given[1:]) and torch.equal(st.next_tokens[0], dense.next_tokens[0])
+    assert out_len[1].tolist() == [4 + A[0] + 1, 0, 9] and (out[1][1:] == -5).all()
+    assert torch.equal(out[1][0], out[0][0])
+    # the first one ends; -1 leaves it out
+    st.err.zero_()
+    M.medusa_pages_free(pages, i32([0, -1, -1, -1]), st.err)
+    y.update(rows=i32([-1, 3, 1]), n_new=i32([0, T, 0, T]))
+    kept = st.next_tokens[0].clone()
+    torch.cuda.synchronize()
+    st.run(y, side_stream=s, append=(out[1], out_len[1]))
+    torch.cuda.synchronize()
+    assert st.err.item() == ROW and st.served.tolist() == [-1, 3, 1]
+    assert st.accept_len.tolist() == [-1, A[1], A[2]]
+    assert torch.equal(st.next_tokens[1:], dense.next_tokens[1:]) and torch.equal(st.next_tokens[0], kept)
+    assert torch.equal(out[1], out[0]) and torch.equal(out_len[1], out_len[0])
+    assert pages.length.tolist() == [0, L + A[2] + 1, 0, L + A[1] + 1]
+
+
+def test_advance_by_itself(M):
+    """Buffers of their own, no output, faults of the acceptance; the largest tree."""
+    g = torch.Generator().manual_seed(2)
+    B, T, K = 16, 512, 8
+    tokens, cand = (torch.randint(0, 1000, (B, T), generator=g, dtype=torch.int32).cuda() for _ in range(2))
+    nodes = torch.randint(0, T, (B, K + 1), generator=g, dtype=torch.int32)
+    nodes[3, 2] = T
+    alen = [b % (K + 1) for b in range(B)]
+    alen[3], alen[5] = 4, K + 1
+    served = [b if b % 4 else -1 for b in range(B)]
+    for with_out in (True, False):
+        err, out, n = i32([0]), torch.full((B, 20), -5, dtype=torch.int32, device="cuda"), i32([b for b in range(B)])
+        nxt, a = torch.zeros(B, T, dtype=torch.int32, device="cuda"), i32(alen)
+        M.medusa_pages_advance(i32(served), tokens, cand, nodes.cuda(), a, nxt, *((out, n) if with_out else (None, None)),
+                               err)
+        torch.cuda.synchronize()
+        assert err.item() == (LENGTH | 2 | CAPACITY if with_out else 0)
+        for b in range(B):
+            on = served[b] >= 0
+            assert torch.equal(nxt[b], (cand if on else tokens)[b]) and a[b] == (alen[b] if on else -1)
+            if not with_out or not on or b in (3, 5) or b + alen[b] + 1 > 20:
+                assert n[b] == b and (out[b] == -5).all() or b == 3
+            else:
+                assert n[b] == b + alen[b] + 1
+                assert torch.equal(out[b, b:b + alen[b] + 1], tokens[b][nodes[b, :alen[b] + 1].long().cuda()])
+    with pytest.raises(M.MedusaError, match="buffer of its own"):
+        M.medusa_pages_advance(i32(served), tokens, nxt, nodes.cuda(), a, nxt)

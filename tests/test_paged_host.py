@@ -200,3 +200,19 @@ def test_device_errors_have_names(M):
     assert [n for v, n in sorted(bits.items())] == ["TOKEN", "NODE", "CAPACITY", "LENGTH", "TIMEOUT", "PAGE", "ROW",
                                                     "LAYOUT"]
     assert sorted(bits) == [1 << k for k in range(len(bits))]
+
+
+@no_gpu
+def test_advance_refusals(M):
+    L = M._lib
+    bufs = [FAKE + 4096 * k for k in range(8)]
+
+    def adv(null=None, B=2, T=20, K=4, cap=30, cand=bufs[2], out=bufs[6], out_len=bufs[7]):
+        p = [bufs[0], bufs[1], cand, bufs[3], bufs[4], bufs[5]]
+        if null is not None:
+            p[null] = None
+        return L.medusa_pages_advance(*p[:5], B, T, K, p[5], out, out_len, cap, None, None)
+
+    assert [adv(null=k) for k in range(6)] == [-1] * 6
+    assert adv(out_len=None) == -1 and adv(cap=0) == -1 and adv(cand=bufs[1]) == -1 and adv(cand=bufs[5]) == -1
+    assert adv(B=0) == -1 and adv(B=17) == -1 and adv(T=0) == -1 and adv(T=513) == -1 and adv(K=9) == -1 and adv(K=-1) == -1
