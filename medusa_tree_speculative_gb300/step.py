@@ -319,11 +319,11 @@ class VerifyStep:
         """Kernels one run() launches: attention 1 (2 for f32), LM head 1,
         acceptance 1, compaction 1, heads 2 with the candidate fill ("fused"),
         or heads 2 ("split"; 1 "joint": W1 runs in the LM head's launch) and
-        candidates 1.  Paged: reserve, served, copy, attention 2 (1 up to 16
-        query rows per key head), compaction 1, commit 1, advance 1 (which
+        candidates 1.  Paged: reserve, served, copy, attention 2 (bf16 up to 16
+        query rows per key head: 1), compaction 1, commit 1, advance 1 (which
         appends the step's tokens as well)."""
         heads = {"fused": 2, "split": 3, "joint": 2}[self.heads]
         if self.cache == "paged":
-            attn = 1 if self.T * (self.w["H"] // self.Hkv) <= 16 else 2
+            attn = 1 if self.w["dtype"] == "bf16" and self.T * (self.w["H"] // self.Hkv) <= 16 else 2
             return 3 + attn + 1 + 1 + 2 + 1 + heads
         return (1 if self.w["dtype"] == "bf16" else 2) + 1 + 1 + 1 + heads

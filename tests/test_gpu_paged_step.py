@@ -173,3 +173,37 @@ def test_step_without_room(M, name, ps):
         assert torch.equal(p[others], q[others])
     old = M.Pages.from_state(before[0], 4, 8, 5, ps)
     assert torch.equal(pages.table[1:], old.table[1:]) and torch.equal(pages.held[1:], old.held[1:])
+
+
+def kernel_nodes(run):
+    """Kernels in the graph that `run(stream)` is captured into."""
+    import ctypes
+
+    g, s = torch.cuda.CUDAGraph(keep_graph=True), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        run(s)
+    cu = ctypes.CDLL("libcuda.so.1")
+    graph, n = ctypes.c_void_p(g.raw_cuda_graph()), ctypes.c_size_t(0)
+    assert cu.cuGraphGetNodes(graph, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cu.cuGraphGetNodes(graph, nodes, ctypes.byref(n)) == 0
+    kernels, kind = 0, ctypes.c_int(0)
+    for node in nodes:
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        kernels += kind.value == 0
+    return kernels
+
+
+@pytest.mark.parametrize("name", ["tiny_fp32", "tiny_bf16"])
+@pytest.mark.parametrize("s,ps", [((2, 2, 2), 16), ((3, 3, 3), 16), ((2, 2, 2), None)])
+def test_launches_per_step(M, name, s, ps):
+    """The kernels of a captured step of the loop, paged (trees of 15 and 40 rows, on both sides of 16) and dense."""
+    from medusa_tree_speculative_gb300 import loop, step
+
+    w = dict(workloads.get(name), tree=("cartesian", s, None))
+    t = M.DeviceTree(step.build_tree(w))
+    lp = loop.DecodeLoop(w, loop.StandInModel(w, seed=3), t, 4, L0=w["L"][0], x0=[5] * w["B"], page_size=ps)
+    side = torch.cuda.Stream()
+    lp.step(side_stream=side)
+    assert kernel_nodes(lambda s: lp.step(s, side_stream=side)) == lp.launches_per_step()
