@@ -760,10 +760,11 @@ size_t medusa_paged_attn_workspace_size(int B, int total_q, int max_new, int H,
  * out: device [total_q][H][Dh].  H a multiple of Hkv, H / Hkv <= 64, Dh 64 or
  * 128, B <= MEDUSA_MAX_ROWS; tensors 16-byte aligned, strides multiples of 16
  * bytes.  A sequence whose row is out of range or was named before
- * (MEDUSA_DEVERR_ROW), with n_b outside 0 .. max_new, another q_start fault or
- * another n_b than the tree's (MEDUSA_DEVERR_LENGTH), whose pages do not cover
- * L + n_b (MEDUSA_DEVERR_CAPACITY) or whose state is broken
- * (MEDUSA_DEVERR_PAGE) is skipped.  A held page outside the pool sets
+ * (MEDUSA_DEVERR_ROW), with n_b outside 0 .. max_new, tokens outside
+ * [0, total_q) or another n_b than the tree's (MEDUSA_DEVERR_LENGTH), whose
+ * pages do not cover L + n_b (MEDUSA_DEVERR_CAPACITY) or whose state is broken
+ * (MEDUSA_DEVERR_PAGE) is skipped.  Where q_start decreases anywhere, all are
+ * (MEDUSA_DEVERR_LENGTH).  A held page outside the pool sets
  * MEDUSA_DEVERR_PAGE; it is not written and reads as zeros.
  * The workspace holds arrival counters: zero-filled (cudaMemset) before its
  * first call, left ready by every call, whatever the next call's sizes (zero

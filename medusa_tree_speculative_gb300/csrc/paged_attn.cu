@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_c
       }
     }
   }
-  __syncthreads();
+  if (__syncthreads_or(starts_decrease<kPrepThreads>(a, t))) return;
   if (a.rows) {  // an entry whose row an earlier one names is skipped
     for (int k = 0; k < nt; ++k) {
       const int b = seq[k];

@@ -87,6 +87,16 @@ MDEV bool seq_info(const PagedAttnArgs& a, int b, SeqInfo& s, int& code) {
   return code == 0 && s.n > 0;
 }
 
+// Whether q_start decreases at one of the sequences that thread t of NT looks at
+// (all of them together: anywhere).  The sequences' tokens are then no longer
+// their own, and the whole call is refused.
+template <int NT>
+MDEV bool starts_decrease(const PagedAttnArgs& a, int t) {
+  bool down = false;
+  for (int b = t; b < a.B; b += NT) down |= a.q_start[b + 1] < a.q_start[b];
+  return down;
+}
+
 // Key tiles of block u (tb tokens per block) of a sequence.
 template <int KT>
 MDEV int unit_tiles(const PagedAttnArgs& a, const SeqInfo& s, int tb, int u) {
@@ -187,7 +197,7 @@ MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& 
     if (lane >= o) x += y;
   }
   if (lane == 31) sc.warp_sum[warp] = x;
-  __syncthreads();
+  const bool refused = __syncthreads_or(starts_decrease<NT>(a, t));
   int64_t before = 0, total = 0;
   for (int w = 0; w < NT / 32; ++w) {
     const int64_t v = sc.warp_sum[w];
@@ -195,6 +205,7 @@ MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& 
     total += v;
   }
   before += x - mine;
+  if (refused) total = 0;
   for (int k = 0; k < per; ++k) {
     const int b = t * per + k;
     if (b < a.B) sc.pre[b] += before;

@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = false;
       code = MEDUSA_DEVERR_ROW;
     }
+    if (__syncthreads_or(starts_decrease<kThreads>(a, tid))) ok = false;  // the sequence where it does reports it
     if (code && sg.head == 0 && rank == 0 && tid == 0) set_err(a.err, code);
     if (!ok) return;  // the whole cluster
     sg.tiles = (sg.s.L + sg.s.n + KT - 1) / KT;

@@ -132,3 +132,40 @@ def test_advance_by_itself(M):
                 assert torch.equal(out[b, b:b + alen[b] + 1], tokens[b][nodes[b, :alen[b] + 1].long().cuda()])
     with pytest.raises(M.MedusaError, match="buffer of its own"):
         M.medusa_pages_advance(i32(served), tokens, nxt, nodes.cuda(), a, nxt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n,far", [([1, 1, 1, 1], 1), ([1] * 40, 1), ([20, 1, 30, 5], 1), ([20, 1, 30, 5], 60)])
+def test_starts_that_decrease(M, dt, n, far):
+    """One start behind the next one's (by one, and past every other): the call is refused whole, since its sequences'
+    tokens overlap or are nobody's; with the start put back it is right."""
+    c = Chunk(M, dt, 4, 2, 128, 16, n, [70] * len(n), gap=2, seed=42)
+    before = c.k.clone(), c.v.clone()
+    good = c.q_start.clone()
+    bits = torch.int16 if dt == "bf16" else torch.int32
+    for at in (1, len(n) - 1):
+        c.q_start[at] = min(int(good[at + 1]) + far, c.total)
+        c.run()
+        torch.cuda.synchronize()
+        assert c.err.item() == LENGTH
+        assert (c.out == 7.0).all()
+        for p, q in zip((c.k, c.v), before):
+            assert torch.equal(p.view(bits), q.view(bits))
+        c.q_start.copy_(good)
+        c.err.zero_()
+    c.go()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [[1, 1, 1], [20, 1, 30]])
+def test_tokens_outside_the_buffers(M, dt, n):
+    """Sequences that begin before the first token or end past the last one are skipped, the others are right."""
+    c = Chunk(M, dt, 4, 2, 128, 16, n, [70, 5, 33], seed=43)
+    before = c.k.clone(), c.v.clone()
+    c.q_start[0] = -1
+    c.q_start[3] = c.total + 1
+    c.max_new += 1
+    c.run()
+    torch.cuda.synchronize()
+    assert c.err.item() == LENGTH
+    c.check(before, skip=(0, 2))
