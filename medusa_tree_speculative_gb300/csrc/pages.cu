@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(kBlock) pages_reserve_kernel(PagesDev p, const
         more = max(0, (int)((end + p.page_size - 1) >> p.shift) - held);
         if (len & (p.page_size - 1)) {
           tail = p.table[(int64_t)t * p.max_pages + (len >> p.shift)];
-          if (!page_ok(p, tail)) code = MEDUSA_DEVERR_PAGE;
-          else refs = p.refs[tail];
+          if (page_ok(p, tail)) refs = p.refs[tail];
+          if (refs < 1) code = MEDUSA_DEVERR_PAGE;  // not a held page: it may be handed out
         }
       }
       if (code) {

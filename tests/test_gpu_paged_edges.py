@@ -169,3 +169,17 @@ def test_tokens_outside_the_buffers(M, dt, n):
     torch.cuda.synchronize()
     assert c.err.item() == LENGTH
     c.check(before, skip=(0, 2))
+
+
+def test_reserve_on_a_free_tail_page(M):
+    """A row whose partly filled tail page has no holder (a broken state): PAGE, not served, so that the call does not
+    hand that page to another row and let both write there."""
+    c = Cache(M, 3, 4, 12, 16)
+    c.reserve([20, 20, 0])
+    c.commit(None, [20, 20, 0])
+    p = int(c.pages.table[0, 1])
+    c.pages.refs[p] = 0
+    c.pages.free_bits[0] |= 1 << p
+    M.medusa_pages_reserve(c.pages, i32([1, 1, 40]), c.copies, c.n_copies, c.granted, c.err)
+    assert c.err.item() == PAGE and c.granted.tolist() == [0, 1, 1] and c.n_copies.item() == 0
+    assert c.pages.held.tolist() == [2, 2, 3] and int(c.pages.table[2, 0]) == p
