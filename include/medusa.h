@@ -749,8 +749,9 @@ size_t medusa_paged_attn_workspace_size(int B, int total_q, int max_new, int H,
  *   k' = RoPE(k_new, pos) and v_new are written at row token L + i;
  *   out = softmax(scale * RoPE(q, pos) . K^T) V over row tokens 0 .. L + i
  *   (causal), or the prefix and L + j for every ancestor-or-self j (tree).
- * RoPE as medusa_tree_attn (pairs (j, j + Dh/2)), the angle exact to 2^-30 of
- * a turn at any position.  The cache is read as it is stored, in its type.
+ * RoPE as medusa_tree_attn (pairs (j, j + Dh/2)); an angle is off by at most
+ * 2^-26 + pos * 2^-53 of a turn (rope_theta >= 1).  The cache is read as it is
+ * stored, in its type.
  * A key that a token does not see has no effect on it, with one limit:
  * non-finite values among a chunk's own v_new may reach other tokens of the
  * same chunk.  A token that sees a NaN score gets NaN, one whose scores are all

@@ -41,9 +41,11 @@ MDEV int64_t page_line(const PagesDev& p, int page, int Hkv, int h, int line) {
 
 // cos and sin of pos * theta^(-2j/Dh).  `turns` is theta^(-2j/Dh) / (2 pi) as a
 // 64-bit binary fraction of a turn, so that pos * turns mod 2^64 is the angle's
-// fraction of a turn, wrapped exactly: the error stays below pos * 2^-56 turns
-// (the fraction comes from a double) at any position, where a float32 product
-// pos * theta^(-2j/Dh) is off by up to pos * 2^-25 radians.
+// fraction of a turn, wrapped exactly, where a float32 product
+// pos * theta^(-2j/Dh) is off by up to pos * 2^-25 radians.  `turns` comes from a
+// power and a quotient of doubles (for theta >= 1 below 0.16 and off by less than
+// 2^-53), and the wrapped fraction is rounded to float32 (at most half a turn
+// either way in 24 bits: 2^-26): 2^-26 + pos * 2^-53 turns in all.
 MDEV void rope_cos_sin(int pos, uint64_t turns, float& c, float& s) {
   const uint64_t f = (uint64_t)(uint32_t)pos * turns;
   const float half_turns = (float)(int32_t)(f >> 32) * 4.656612873077393e-10f;  // 2^-31: [-1, 1) half turns

@@ -183,3 +183,67 @@ def test_reserve_on_a_free_tail_page(M):
     M.medusa_pages_reserve(c.pages, i32([1, 1, 40]), c.copies, c.n_copies, c.granted, c.err)
     assert c.err.item() == PAGE and c.granted.tolist() == [0, 1, 1] and c.n_copies.item() == 0
     assert c.pages.held.tolist() == [2, 2, 3] and int(c.pages.table[2, 0]) == p
+
+
+def turn_fractions(pos, theta, D):
+    """pos * theta^(-2j/D) / (2 pi) mod 1 for every j, from 60 decimal digits."""
+    import decimal
+
+    with decimal.localcontext() as ctx:
+        ctx.prec = 60
+        two_pi = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+        lg = decimal.Decimal(theta).ln()
+        return [float((pos * (-2 * j * lg / D).exp() / two_pi) % 1) for j in range(D // 2)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [5, 2 ** 20 + 3, 2 ** 24 + 1, 2 ** 28 - 40])
+def test_angles_at_far_positions(M, dt, L):
+    """Up to the longest row a cache may hold (2^28 tokens, its pages all one and the same but the last): the rotation
+    of the appended keys, and the result."""
+    import math
+
+    D, ps, n, theta = 64, 256, 3, 10000.0
+    ty = torch.bfloat16 if dt == "bf16" else torch.float32
+    most = 2 ** 28 // ps
+    p = M.Pages(1, most, 2, ps)
+    held = -(-(L + n) // ps)
+    p.table[0, :held] = 0
+    first = L // ps  # the chunk's page is the row's own
+    p.table[0, first:held] = 1
+    assert held - first == 1
+    p.length[0], p.held[0] = L, held
+    g = torch.Generator(device="cuda").manual_seed(44)
+    k, v = (torch.randn(2, 1, ps, D, generator=g, device="cuda").to(ty) for _ in range(2))
+    q, kn, vn = (torch.randn(n, 1, D, generator=g, device="cuda").to(ty) for _ in range(3))
+    out, err = torch.zeros(n, 1, D, dtype=ty, device="cuda"), i32([0])
+    ws = torch.zeros(M.medusa_paged_attn_workspace_size(1, n, n, 1, 1, D, ty), dtype=torch.uint8, device="cuda")
+    M.medusa_paged_attn(q, kn, vn, k, v, p, None, i32([0, n]), n, None, theta, D ** -0.5, out, ws, err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    u = torch.finfo(ty).eps / 2
+
+    def turned(x, i):
+        f = torch.tensor(turn_fractions(L + i, theta, D), dtype=torch.float64, device="cuda") * (2 * math.pi)
+        a, b = x[i, 0, :D // 2].double(), x[i, 0, D // 2:].double()
+        return torch.cat([a * f.cos() - b * f.sin(), b * f.cos() + a * f.sin()]), (a.abs() + b.abs()).repeat(2)
+
+    for i in range(n):
+        want, size = turned(kn, i)
+        got = k[1, 0, (L + i) % ps].double()
+        # the angle; sine and cosine to two units in the last place, two products and a sum; the cache's rounding
+        angle = 2 * math.pi * (2.0 ** -26 + (L + i) * 2.0 ** -53)
+        assert ((got - want).abs() <= (angle + 2.0 ** -23 + 2 * 2.0 ** -24) * size + u * want.abs()).all(), i
+        assert torch.equal(v[1, 0, (L + i) % ps], vn[i, 0])
+        # a page's key counts as often as the row holds it
+        kk = torch.cat([k[0, 0], k[1, 0, :(L + i) % ps + 1]]).double()
+        vv = torch.cat([v[0, 0], v[1, 0, :(L + i) % ps + 1]]).double()
+        times = torch.cat([torch.full((ps,), float(first), device="cuda", dtype=torch.float64),
+                           torch.ones((L + i) % ps + 1, device="cuda", dtype=torch.float64)])
+        z = kk @ turned(q, i)[0] * D ** -0.5 + times.log()
+        w = torch.softmax(z, -1)
+        # scores to 2^-18 (a bf16 query's two parts, 64 products, the angle's 2^-22); a CTA's share of tiles (of 64
+        # keys, 152 CTAs at the least), added one after the other to sums and normaliser; the result's rounding
+        tiles = (L + n) / 64 / 152 + 2
+        tol = (2.0 ** -16 + 2 * tiles * 2.0 ** -24) * (w @ vv.abs()) + u * (w @ vv).abs()
+        assert ((out[i, 0].double() - w @ vv).abs() <= tol).all(), i
