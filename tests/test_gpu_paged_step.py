@@ -207,3 +207,70 @@ def test_launches_per_step(M, name, s, ps):
     side = torch.cuda.Stream()
     lp.step(side_stream=side)
     assert kernel_nodes(lambda s: lp.step(s, side_stream=side)) == lp.launches_per_step()
+
+
+@pytest.mark.parametrize("name,H,Hkv,s,side", [("tiny_bf16", 8, 2, (3, 3, 3), True), ("tiny_bf16", 2, 1, (2, 2, 2), False),
+                                               ("tiny_fp32", 4, 2, (2, 2, 2), True), ("tiny_bf16", 16, 1, (1,), False)])
+def test_step_with_grouped_heads(M, name, H, Hkv, s, side):
+    """Query heads that share key heads (w["Hkv"]), two sequences of different lengths: the attention against 64-bit
+    formulas, the accepted path's keys and values in place."""
+    from medusa_tree_speculative_gb300 import step
+
+    ps, L = 16, [21, 300]
+    w = dict(workloads.get(name), B=2, H=H, Hkv=Hkv, L=L, tree=("cartesian", s, None))
+    if len(s) < w["K"]:
+        w["K"] = len(s)
+    w["Dh"] = w["d"] // H if w["d"] // H in (64, 128) else 64
+    tree = M.DeviceTree(step.build_tree(w))
+    T, Dh = tree.T, w["Dh"]
+    ty = step.TORCH_DT[w["dtype"]]
+    x = {k: to_dev(v) for k, v in synth.make_step(w, T, 8).items()}
+    wts = {k: (None if v is None else to_dev(v)) for k, v in synth.make_weights(w, 8).items()}
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x["k_new"], x["v_new"] = (torch.randn(2, T, Hkv, Dh, generator=g, device="cuda").to(ty) for _ in range(2))
+    new = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    st = step.VerifyStep(w, wts, tree, max_prefix=max(L), cache="paged")
+    pages = M.Pages(3, 40, 60, ps)
+    pools = [torch.full((60, Hkv, ps, Dh), float("nan"), dtype=ty, device="cuda") for _ in range(2)]
+    M.medusa_pages_reserve(pages, new([L[0], 0, L[1]]), st.copies, st.n_copies, None, st.err)
+    M.medusa_pages_commit(pages, None, new([L[0], 0, L[1]]), 0, st.err)
+    rows = [2, 0]
+    prefix = []
+    for b, r in enumerate(rows):
+        n = int(pages.length[r])
+        i = torch.arange(n, device="cuda")
+        kv = [torch.randn(n, Hkv, Dh, generator=g, device="cuda").to(ty) for _ in range(2)]
+        for pool, y in zip(pools, kv):
+            pool[pages.table[r, i // ps].long(), :, i % ps] = y
+        prefix.append(kv)
+    side_stream = torch.cuda.Stream() if side else None
+    torch.cuda.synchronize()
+    st.run(dict(x, k_pages=pools[0], v_pages=pools[1], pages=pages, rows=new(rows), n_new=new([T, 0, T])),
+           side_stream=side_stream)
+    torch.cuda.synchronize()
+    assert st.err.item() == 0 and st.served.tolist() == rows
+    host, u = tree.host, half_step(ty)
+    anc = torch.from_numpy(((host.anc_mask[:, np.arange(T) // 32] >> (np.arange(T) % 32).astype(np.uint32)) & 1) != 0)
+    for b, r in enumerate(rows):
+        n = prefix[b][0].shape[0]
+        pos = n + torch.from_numpy(host.depth).cuda().long()
+        seen = torch.cat([torch.ones(T, n, dtype=torch.bool, device="cuda"), anc.cuda()], 1)
+        q = rotate(x["q"][b].double(), pos, 10000.0)
+        kt = rotate(x["k_new"][b].double(), pos, 10000.0)
+        for h in range(H):
+            hk = h // (H // Hkv)
+            want, tol = attention(q[:, h], torch.cat([prefix[b][0][:, hk].double(), kt[:, hk].to(ty).double()]),
+                                  torch.cat([prefix[b][1][:, hk], x["v_new"][b, :, hk]]).double(), seen, Dh ** -0.5, u,
+                                  n + T + Dh + 64)
+            # a key's rounding to the cache's type may fall the other way
+            assert ((st.out[b, :, h].double() - want).abs() <= 2 * tol).all(), (b, h)
+        A = int(st.accept_len[b])
+        path = st.accepted_nodes[b, :A + 1].long()
+        assert int(pages.length[r]) == n + A + 1
+        i = torch.arange(n + A + 1, device="cuda")
+        at = pages.table[r, i // ps].long(), i % ps
+        k, v = pools[0][at[0], :, at[1]], pools[1][at[0], :, at[1]]
+        assert torch.equal(v, torch.cat([prefix[b][1], x["v_new"][b, path]])) and torch.equal(k[:n], prefix[b][0])
+        size = x["k_new"][b, path].double().abs()
+        size = size + size.roll(Dh // 2, -1)
+        assert ((k[n:].double() - kt[path]).abs() <= u * kt[path].abs() + 2.0 ** -21 * size).all()
