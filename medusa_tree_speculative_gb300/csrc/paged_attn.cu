@@ -80,7 +80,9 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_c
       }
     }
   }
-  if (__syncthreads_or(starts_decrease<kPrepThreads>(a, t))) return;
+  bool down = false;  // looked up beside the first warp's search
+  for (int b = t - 32; t >= 32 && b < a.B; b += kPrepThreads - 32) down |= starts_decrease(a, b);
+  if (__syncthreads_or(down)) return;
   if (a.rows) {  // an entry whose row an earlier one names is skipped
     for (int k = 0; k < nt; ++k) {
       const int b = seq[k];

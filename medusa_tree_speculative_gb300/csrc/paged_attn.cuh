@@ -61,9 +61,12 @@ struct PagedAttnArgs {
 
 // Sequence b: its row, tokens and prefix; false (and an error code, 0 where it
 // merely has no tokens) if it is skipped.
+// Where q_start decreases at any sequence, the tokens of the others are no longer
+// their own either, and the whole call is refused: `starts_decrease`.
 struct SeqInfo {
   int row, q0, n, L;
 };
+MDEV bool starts_decrease(const PagedAttnArgs& a, int b) { return a.q_start[b + 1] < a.q_start[b]; }
 MDEV bool seq_info(const PagedAttnArgs& a, int b, SeqInfo& s, int& code) {
   code = 0;
   s.q0 = a.q_start[b];
@@ -85,16 +88,6 @@ MDEV bool seq_info(const PagedAttnArgs& a, int b, SeqInfo& s, int& code) {
   if (!row_state_ok(a.p, s.L, held)) code = MEDUSA_DEVERR_PAGE;
   else if ((int64_t)s.L + s.n > (int64_t)held * a.p.page_size) code = MEDUSA_DEVERR_CAPACITY;
   return code == 0 && s.n > 0;
-}
-
-// Whether q_start decreases at one of the sequences that thread t of NT looks at
-// (all of them together: anywhere).  The sequences' tokens are then no longer
-// their own, and the whole call is refused.
-template <int NT>
-MDEV bool starts_decrease(const PagedAttnArgs& a, int t) {
-  bool down = false;
-  for (int b = t; b < a.B; b += NT) down |= a.q_start[b + 1] < a.q_start[b];
-  return down;
 }
 
 // Key tiles of block u (tb tokens per block) of a sequence.
@@ -143,7 +136,7 @@ struct PlanScratch {
 };
 struct Plan {
   uint32_t valid[MEDUSA_MAX_ROWS / 32];  // the sequences that are not skipped
-  int64_t total;                         // places in all
+  int64_t total;                         // places in all (negative: refused)
 };
 
 // Where in the list a CTA stands: a unit and the tiles of it that are its own.
@@ -189,6 +182,7 @@ MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& 
       atomicOr(&pl.valid[b >> 5], 1u << (b & 31));
       mine += (int64_t)a.Hkv * seq_places<KT, EC>(a, s, tb);
     }
+    if (starts_decrease(a, b)) mine -= 1ll << 52;  // the call is refused: no places are as many, the sum is negative
   }
   int64_t x = mine;
 #pragma unroll
@@ -197,7 +191,7 @@ MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& 
     if (lane >= o) x += y;
   }
   if (lane == 31) sc.warp_sum[warp] = x;
-  const bool refused = __syncthreads_or(starts_decrease<NT>(a, t));
+  __syncthreads();
   int64_t before = 0, total = 0;
   for (int w = 0; w < NT / 32; ++w) {
     const int64_t v = sc.warp_sum[w];
@@ -205,7 +199,6 @@ MDEV void make_plan(const PagedAttnArgs& a, PlanScratch& sc, Plan& pl, int64_t& 
     total += v;
   }
   before += x - mine;
-  if (refused) total = 0;
   for (int k = 0; k < per; ++k) {
     const int b = t * per + k;
     if (b < a.B) sc.pre[b] += before;

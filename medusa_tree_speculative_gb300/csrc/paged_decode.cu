@@ -157,7 +157,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     sg.u = 0;
     sg.m = 1;
     sg.unit_x = 0;
-    int code;
+    int code, start0 = 0, start1 = 0;  // thread b looks at sequence b: at most a unit per two SMs
+    if (tid < a.B) {
+      start0 = a.q_start[tid];
+      start1 = a.q_start[tid + 1];
+    }
     bool ok = seq_info(a, sg.b, sg.s, code), twice = false;
     if (a.rows && ok)
       for (int j = tid; j < sg.b; j += kThreads) twice |= a.rows[j] == sg.s.row && a.q_start[j + 1] > a.q_start[j];
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = false;
       code = MEDUSA_DEVERR_ROW;
     }
-    if (__syncthreads_or(starts_decrease<kThreads>(a, tid))) ok = false;  // the sequence where it does reports it
+    if (__syncthreads_or(start1 < start0)) ok = false;  // the sequence where they decrease reports it
     if (code && sg.head == 0 && rank == 0 && tid == 0) set_err(a.err, code);
     if (!ok) return;  // the whole cluster
     sg.tiles = (sg.s.L + sg.s.n + KT - 1) / KT;
@@ -559,7 +563,7 @@ constexpr int kClusterTiles = 16;
 template <int DH>
 int run_any(const PagedAttnArgs& a, const PagedKernels& k) {
   const int64_t units = (int64_t)a.B * a.Hkv, tiles = ((int64_t)a.p.max_pages * a.p.page_size + KT - 1) / KT;
-  const int cl = units * 8 <= k.sms ? 8 : units * 4 <= k.sms ? 4 : units * 2 <= k.sms ? 2 : 1;
+  const int cl = a.B > kThreads ? 1 : units * 8 <= k.sms ? 8 : units * 4 <= k.sms ? 4 : units * 2 <= k.sms ? 2 : 1;
   if (cl > 1 && tiles <= (int64_t)kClusterTiles * cl) {
     if (cl == 8) return run<DH, 8>(a, k);
     return cl == 4 ? run<DH, 4>(a, k) : run<DH, 2>(a, k);
