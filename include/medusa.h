@@ -669,7 +669,8 @@ int medusa_pages_reserve(const medusa_pages_t* pages, const int32_t* n_new,
 /* served[b] = rows[b] (rows NULL: b) where granted (medusa_pages_reserve's)
  * says that the row has its room, else -1, b < B: as `rows` of the calls below
  * it makes them skip the sequences without room (MEDUSA_DEVERR_ROW), which
- * would otherwise write into pages that they may share.  rows, served: device
+ * would otherwise write into pages that they may share.  The error word does not
+ * tell a sequence left out from a bad row; served does.  rows, served: device
  * [B]; granted: device [pages->rows]. */
 int medusa_pages_served(const medusa_pages_t* pages, const int32_t* rows,
                         const int32_t* granted, int B, int32_t* served,
@@ -755,7 +756,11 @@ size_t medusa_paged_attn_workspace_size(int B, int total_q, int max_new, int H,
  * A key that a token does not see has no effect on it, with one limit:
  * non-finite values among a chunk's own v_new may reach other tokens of the
  * same chunk.  A token that sees a NaN score gets NaN, one whose scores are all
- * minus infinity gets zeros.
+ * minus infinity gets zeros; in bf16 an infinite query, or key that is seen, may
+ * make a score NaN that the formula has infinite.
+ * bf16: the result is rounded once; queries, and weights up to 128 rows (tokens
+ * x heads) per key head, are held to 2^-16; the weights of longer chunks are
+ * rounded to bf16.  Everything else has 32 bits.
  * length stays (medusa_pages_commit); the pages for L + n_b tokens must be
  * there and the last ones the row's own (medusa_pages_reserve).
  * out: device [total_q][H][Dh].  H a multiple of Hkv, H / Hkv <= 64, Dh 64 or

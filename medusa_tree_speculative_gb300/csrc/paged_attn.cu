@@ -16,10 +16,11 @@ namespace {
 // scale in them (bf16: rounded, and in a second plane what the rounding left,
 // rounded), keys and values to their pages.  Every element is read and
 // written once: bound by memory for long chunks (16 tokens per CTA, all heads:
-// 8192 tokens of 48 heads, 201 MB, in 37 us), by the latency of a thread's few steps
-// for short ones (4 tokens, as many groups of heads as give a thread
-// kPrepSteps).  16 against 4 tokens per CTA, with the attention: 392 and 396 us
-// for 8192 tokens; 132 and 100 us for 260.
+// 8192 tokens of 48 heads, 268 MB, in 58 us on cold caches), by the latency of a
+// thread's few steps for short ones (4 tokens, as many groups of heads as give a
+// thread kPrepSteps).  16 against 4 tokens per CTA, with the attention: 999 and
+// 1030 us for 32768 tokens of 4 heads, 572 and 571 for 8192 of 32 heads; 51 and
+// 40 us for 260 of 32.
 constexpr int kPrepThreads = 256;
 constexpr int kPrepSteps = 4;
 
@@ -192,14 +193,15 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const __grid_c
 // A tile's sums are added to the row's once (error against 64 bits at 60000 keys:
 // 4.2e-7, 2-norm; 2.7e-6 with one running sum over the keys).
 // Bound by shared memory and by the barriers between a tile's four phases: the
-// FMA pipe is 41% busy (4 x 8 and 8 x 8 products per thread need fewer loads but
+// FMA pipe is 43% busy (4 x 8 and 8 x 8 products per thread need fewer loads but
 // leave fewer warps, and gain nothing; nor do two FMAs per instruction).  345
 // tokens in five sequences, 16 heads of 64 (four per key head), prefixes up to
-// 2000: 74 us with the rotation's launch.  Blocks of at most 16 rows have a form
+// 2000: 75 us with the rotation's launch.  Blocks of at most 16 rows have a form
 // of their own where the call has no others: one token at a prefix of 1024, 32
-// heads of 128, 22.6 us against 28.7 in the form for 64 rows; 64 tokens, 16
-// heads of 128 (four per key head), prefixes up to 4000, 144 against 160.
-constexpr int kGenThreads = 256, kGenCtas = 2;  // CTAs per SM (the two cases above: 74 and 144 us; with 3: 89, 186)
+// heads of 128, 24.8 us against 30.8 in the form for 64 rows; 64 tokens, 16
+// heads of 128 (four per key head), prefixes up to 4000, 144 against 161.
+// CTAs per SM (the 345 and the 64 tokens): 75 and 144 us; with 1, 85 and 198; with 3, 83 and 190.
+constexpr int kGenThreads = 256, kGenCtas = 2;
 
 template <int DH, int RB, int KT>
 struct Gen {
@@ -646,8 +648,8 @@ extern "C" int medusa_paged_attn(const void* q, int64_t q_stride, const void* k_
   // launches, one per kind, took 14% longer for eleven sequences of 1 .. 700
   // tokens (40 heads of 64, prefixes up to 5000).  Up to kFewRows rows per key
   // head the kernels for few rows are ahead: 64 single tokens with four heads
-  // per key head and prefixes up to 8192 take 187 us, 205 us in the other one;
-  // one token at a prefix of 1024, 11.7 and 24.6 us.
+  // per key head and prefixes up to 8192 take 185 us, 246 us in the other one;
+  // one token at a prefix of 1024, 12 and 24 us.
   const bool few = (int64_t)max_new * a.g <= kFewRows;
   a.counters = reinterpret_cast<int*>(ws) + (few ? 0 : kPagedCounters);
   a.part = reinterpret_cast<float*>(ws + w.part);

@@ -15,7 +15,8 @@
 //     over them in tensor memory, with no exchange between threads.  (Two
 //     threads per row, which agree on the maximum through shared memory, take
 //     less time from scores to P, but issue 1.7 times the instructions, and the
-//     MMA warp shares the issue slots: 4% longer for 8192 tokens.)
+//     MMA warp shares the issue slots: 4% longer for 8192 tokens, with queries
+//     in one part.)
 //   * O stays in tensor memory.  The base m of a row only moves when the
 //     row's maximum passes it by more than 8 (P is at most 2^8, its sum is
 //     kept in 32 bits), so O is rescaled a few times per row and not per tile.
@@ -27,25 +28,27 @@
 // Queries come rotated and scaled from the launch before this one, which also
 // appends the chunk, as two bf16 parts, high and low, 2^-16 relative together:
 // an error of a query is one of every score, and grows with the scores.  Each
-// part has a product of its own.  (One part alone takes 361 us in place of 520
-// for 8192 tokens of heads of 128, and its error, at scores of deviation 1, is
-// as large as the result's own rounding.)  The low parts take the room that tiles of
-// 128 keys would need at Dh = 128.
+// part has a product of its own.  (One part alone takes 363 us in place of 488
+// for 8192 tokens of 32 heads of 128, and its error, at scores of deviation 1, is
+// as large as the result's own rounding.)  The low parts take the room that
+// tiles of 128 keys would need at Dh = 128.
 // P is rounded once to bf16 where a call has two query tiles: a relative 2^-8 a
 // weight at most, independent from key to key, so no larger in the result than
-// its own rounding, whatever the scores.  (In two parts: 100 us in place of 79
-// for the mixed batch below, 540 in place of 361 for the prompt, both with queries
-// in one.)  A call with one query tile, bound by memory, has time for two
-// parts of P as well (4 of its 110 us).
+// its own rounding, whatever the scores.  (In two parts, with queries in one: 104
+// us in place of 79 for the mixed batch below, 579 in place of 412 for the
+// prompt, and as far from 64 bits as this way round.)  A call with one query
+// tile, bound by memory, has time for two parts of P as well (4 of its 110 us).
 // MMAs that one thread issues run in issue order on the CTA's tensor core:
 // QK(j+1) may overwrite the columns from which PV(j), issued before it, reads
 // P.
 // Measured, with the launch before it: 8192 tokens of 32 heads of 128 (8 key
-// heads) 564 us, 1.46 PFLOP/s with both parts' products; trees of 65 rows on
-// four prefixes up to 8192, 52 heads of 128, 110 us (bound by memory in the
-// loop over tiles; plan, first loads and joins around it); eleven sequences of
-// 1 .. 700 tokens, 40 heads of 64 (8 key heads), prefixes up to 5000, 88 us
-// (bound by the way from one tile's scores to the next one's).
+// heads) 564 to 573 us, the kernel itself 488 us or 1.69 PFLOP/s with both parts'
+// products, 97% of what a library product sustains, at the power limit (SM clock
+// 1950 MHz; 2070 for the others); trees of 65 rows on four prefixes up to 8192, 52
+// heads of 128, 111 us (bound by memory in the loop over tiles; plan, first loads
+// and joins around it); eleven sequences of 1 .. 700 tokens, 40 heads of 64 (8 key
+// heads), prefixes up to 5000, 88 us (bound by the way from one tile's scores to
+// the next one's).
 #include <utility>
 
 #include "paged_attn.cuh"
@@ -62,7 +65,7 @@ constexpr int kCost = 2;  // 8192 tokens: 585, 565, 565 us at 1, 2, 3; the mixed
 constexpr int kThreads = 384;  // two softmax groups of 128; the load warp, the MMA warp and two segment warps
 constexpr int kSoft = 256, kLoadWarp = 8, kMmaWarp = 9;
 // Registers: the block starts with 168 a thread (384 x 168 = 64512); the softmax
-// threads, which hold 128 scores, then take what the other warps give up:
+// threads, which hold up to 128 scores, then take what the other warps give up:
 // 256 x 208 + 128 x 88.
 constexpr int kLaunchRegs = 168, kSoftRegs = 208, kOtherRegs = 88;
 static_assert(kSoft * kSoftRegs + (kThreads - kSoft) * kOtherRegs <= kThreads * kLaunchRegs, "registers");
@@ -81,7 +84,8 @@ struct Half {
 };
 
 // NARROW: a call whose chunks all have one query tile (at most 128 rows per key
-// head), bound by memory: the second tile's place goes to the ring.
+// head), bound by memory: the second tile's place goes to the ring (the trees
+// above, 2% less time than without).
 template <int DH, bool NARROW>
 struct Cfg {
   static constexpr int kHalves = DH / 64;

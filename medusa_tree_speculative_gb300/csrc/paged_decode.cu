@@ -23,11 +23,11 @@
 // Small calls are bound by latency.  Where every row's pages hold few tiles and
 // there are SMs to spare, a cluster of CL CTAs takes a unit instead: no list to
 // plan, and the join goes through distributed shared memory in place of the
-// workspace and its counters (one token at a prefix of 1024, 32 heads: 11.7 us
+// workspace and its counters (one token at a prefix of 1024, 32 heads: 11.9 us
 // against 16.4).
-// Measured: 64 tokens with prefixes of 500 .. 8192, 32 heads of 128 on 8 key
-// heads, 184 us, 5.96 TB/s (171 with pages of 32 tokens or more: half as
-// many copies).
+// Measured (SM clock 2070 MHz): 64 tokens with prefixes of 500 .. 8192, 32 heads
+// of 128 on 8 key heads, 181 to 185 us, 6.0 TB/s (174 to 177 with pages of 32
+// tokens or more: half as many copies).
 #include "cluster.cuh"
 #include "paged_attn.cuh"
 #include "sm100.cuh"

@@ -11,8 +11,8 @@
 // of 1024 threads takes (65536 pages are 2048 words, two per thread): what
 // bounds it is the latency of a few dependent loads and block barriers, not
 // bytes (compact's plan 5 us).  reserve hands out its few pages there as well
-// (12 us for 420 rows); compact leaves table, counts and list to all SMs (7 us).
-// fork and free run a CTA per row (7 us for 256 and 420 rows).  copy moves 16
+// (15 us for 420 rows); compact leaves table, counts and list to all SMs (7 us).
+// fork and free run a CTA per row (7 to 8 us for 256 and 420 rows).  copy moves 16
 // bytes per thread, eight loads in flight, and is bound by memory: 16384 pages
 // of 64 KB in 321 us, 6.7 TB/s.
 #include "internal.h"
