@@ -879,9 +879,8 @@ size_t medusa_paged_attn_shared_workspace_size(int B, int n_groups,
  * MEDUSA_DEVERR_LENGTH).  Sharing has its price in launches: a call whose B rows are
  * too short to save as much reading (by max_pages; 128 MB for single tokens) does not
  * look at its groups, and fewer than 128 common tokens are not shared.  Other arguments, results, errors and the workspace's rules
- * are medusa_paged_attn's; the limit on non-finite values holds for one sequence's
- * tokens, as there.  With more than 128 rows (tokens x heads) per key head in all
- * groups, the weights of common tokens are rounded to bf16. */
+ * are medusa_paged_attn's, its roundings too (the weights go by max_new there and
+ * here); the limit on non-finite values holds for one sequence's tokens, as there. */
 int medusa_paged_attn_shared(const void* q, int64_t q_stride,
                              const void* k_new, int64_t k_stride,
                              const void* v_new, int64_t v_stride,

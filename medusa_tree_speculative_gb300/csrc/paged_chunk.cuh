@@ -38,6 +38,12 @@
 // us in place of 79 for the mixed batch below, 579 in place of 412 for the
 // prompt, and as far from 64 bits as this way round.)  A call with one query
 // tile, bound by memory, has time for two parts of P as well (4 of its 110 us).
+// Behind a shared prefix the rows of a group are those of many sequences: where each
+// has at most 128, kCommon holds P in two parts however many there are (FINE), so
+// that a token's weights are as exact as without sharing, whoever shares with it
+// (104 tokens behind up to 16384, 32 heads of 128 on 8: error against 64 bits 0.0023
+// to 0.0017, its own rounding, for 167 to 174 us; 120 tokens behind up to 12000, 64
+// heads of 64, 111 to 128 us).
 // MMAs that one thread issues run in issue order on the CTA's tensor core:
 // QK(j+1) may overwrite the columns from which PV(j), issued before it, reads
 // P.
@@ -203,7 +209,7 @@ MDEV void umma_ts_words(uint32_t d, uint32_t a, uint32_t blo, uint32_t hi, uint3
 // The products of lane I with the keys or values in stage B (QT: the query
 // tile).  Matrix descriptors: 128-byte swizzle, 1024 bytes between 8-row
 // groups; low word address / 16 and, for V, the bytes / 16 between its halves.
-template <int DH>
+template <int DH, bool FINE>
 struct Products {
   using G = ChunkCfg<DH, false, kAll>;  // tiles and stages do not depend on the keys
   static constexpr uint64_t kHi = (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32;
@@ -220,10 +226,11 @@ struct Products {
                 kHi | (kK + B * 2 * kTile16 + step(KK, kHalf16)), idesc_bf16_f32(128, KT), PART != 0 || KK != 0>(),
      ...);
   }
+  // (steps past KT / 16: P's low parts)
   template <uint32_t I, uint32_t B, int... J>
   static MDEV void pv_steps(uint32_t add, std::integer_sequence<int, J...>) {
     // V as stored, keys x values, is MN-major
-    (umma_ts_const<256 + I * 128, I * 128 + J * 8, kHi | (kV + B * 2 * kTile16 + J * (2048 >> 4)),
+    (umma_ts_const<256 + I * 128, I * 128 + J * 8, kHi | (kV + B * 2 * kTile16 + J % (KT / 16) * (2048 >> 4)),
                    idesc_bf16_f32(128, DH) | 1u << 16>(J == 0 ? add : 1u),
      ...);
   }
@@ -234,7 +241,7 @@ struct Products {
   }
   template <uint32_t I, uint32_t B>
   static MDEV void pv(uint32_t add) {
-    pv_steps<I, B>(add, std::make_integer_sequence<int, KT / 16>());
+    pv_steps<I, B>(add, std::make_integer_sequence<int, (FINE ? 2 : 1) * KT / 16>());
   }
 };
 
@@ -262,12 +269,14 @@ MDEV void wait_at(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   *abort_flag = 1;
 }
 
-template <int DH, bool NARROW, Keys KEYS>
+// FINE: P in two parts.
+template <int DH, bool NARROW, bool FINE, Keys KEYS>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQl,
                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ PagedAttnArgs a) {
   using G = ChunkCfg<DH, NARROW, KEYS>;
+  static_assert(FINE || !NARROW, "a call with one query tile has time for both parts");
   constexpr int KT = G::KT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -461,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_at(kDone, 0, abort_flag);
         }
       } else if (elect_one()) {
-        using P = Products<DH>;
+        using P = Products<DH, FINE>;
         uint32_t t = 0, ph0 = 0, ph1 = 0, qph = 0;  // the CTA's tiles so far; phases of p_full and q_full
         uint32_t nt = sg.t1 - sg.t0, wide = min(tb, sg.s.n - sg.u * tb) * a.g > 128;
         bool ready = false;  // the segment's first scores are on their way
@@ -722,10 +731,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               w = ex2(w);
               add2(sa[e & 1], sb[e & 1], u, w);
               p[e] = pack2_bf16(u, w);
-              if (NARROW) low[e] = pack2_bf16(u - __uint_as_float(p[e] << 16), w - __uint_as_float(p[e] & 0xffff0000u));
+              if (FINE) low[e] = pack2_bf16(u - __uint_as_float(p[e] << 16), w - __uint_as_float(p[e] & 0xffff0000u));
             }
             tmem_st_32x32b_x16(tS + h * 16, p);
-            if (NARROW) tmem_st_32x32b_x16(tS + KT / 2 + h * 16, low);
+            if (FINE) tmem_st_32x32b_x16(tS + KT / 2 + h * 16, low);
           }
           l += (sa[0] + sb[0]) + (sa[1] + sb[1]);
           tmem_st_wait();
@@ -939,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && *abort_flag) set_err(a.err, MEDUSA_DEVERR_TIMEOUT);
 }
 
-template <int DH, bool NARROW, Keys KEYS>
+template <int DH, bool NARROW, bool FINE, Keys KEYS>
 int run_chunk(const PagedAttnArgs& a, const PagedKernels& k) {
   CUtensorMap tmQ, tmQl, tmK, tmV;
   const int most = key_box(ChunkCfg<DH, NARROW, KEYS>::KT), box = a.p.page_size < most ? a.p.page_size : most;
@@ -947,7 +956,7 @@ int run_chunk(const PagedAttnArgs& a, const PagedKernels& k) {
   if (!make_rows_map(&tmQ, a.q_rot, rows, DH, 128) ||
       !make_rows_map(&tmQl, static_cast<uint16_t*>(a.q_rot) + a.q_low, rows, DH, 128) || !make_pool_map(&tmK, a.k_pages, a, DH, box) || !make_pool_map(&tmV, a.v_pages, a, DH, box))
     return fail(MEDUSA_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", k.name);
-  auto* fn = paged_chunk_kernel<DH, NARROW, KEYS>;
+  auto* fn = paged_chunk_kernel<DH, NARROW, FINE, KEYS>;
   static std::atomic<uint64_t> done{0};
   // the registers' redistribution would wait for ever if the block had fewer to give
   if (int rc = prepare_kernel(reinterpret_cast<const void*>(fn), ChunkCfg<DH, NARROW, KEYS>::smem, kLaunchRegs, kSmemBase, &done,
@@ -964,8 +973,12 @@ template <Keys KEYS>
 int launch_paged_chunk(const PagedAttnArgs& a, int Dh, const PagedKernels& k) {
   // a group's rows are those of all its sequences
   if ((int64_t)(KEYS == kCommon ? a.total_q : a.max_new) * a.g <= 128)
-    return Dh == 64 ? chunk::run_chunk<64, true, KEYS>(a, k) : chunk::run_chunk<128, true, KEYS>(a, k);
-  return Dh == 64 ? chunk::run_chunk<64, false, KEYS>(a, k) : chunk::run_chunk<128, false, KEYS>(a, k);
+    return Dh == 64 ? chunk::run_chunk<64, true, true, KEYS>(a, k) : chunk::run_chunk<128, true, true, KEYS>(a, k);
+  // the others of a group do not make a sequence's weights less exact
+  if constexpr (KEYS == kCommon)
+    if ((int64_t)a.max_new * a.g <= 128)
+      return Dh == 64 ? chunk::run_chunk<64, false, true, KEYS>(a, k) : chunk::run_chunk<128, false, true, KEYS>(a, k);
+  return Dh == 64 ? chunk::run_chunk<64, false, false, KEYS>(a, k) : chunk::run_chunk<128, false, false, KEYS>(a, k);
 }
 
 }  // namespace medusa
