@@ -575,10 +575,12 @@ int medusa_accept_rejection(const float* logits, const float* draft_logits,
  *          of theirs, at least one (1: all);
  *   min_p  of those the ones with w >= min_p (0: all).
  * token[r] is the first kept one, in vocabulary order, at which the running sum of
- * the kept weights passes uniforms[r] times their sum; logp[r] (nullable) its log
+ * the kept weights passes uniforms[r] times their sum (0: the first kept one whose
+ * weight is not 0 in 64 bits, however small it is); logp[r] (nullable) its log
  * probability among the kept ones, kept[r] (nullable) their number.  temperature 0
  * takes the first token of the order (kept 1, logp 0).  A logit of minus infinity is
- * no token.  The sums that decide are exact to 2^-28 of each weight, so that the
+ * no token.  The sums that decide are exact to 2^-27 of each weight and, for each
+ * token, 2^-44 of the largest weight (one below 2^-45 of it adds nothing), so that the
  * tokens are those of the formula in 64 bits but where two sums agree that closely.
  * A row with a NaN or plus infinity, or with nothing but minus infinity, or with a
  * setting outside its range (temperature >= 0 and finite, top_p, min_p in [0, 1])

@@ -8,12 +8,16 @@
 // decided by sums over up to the whole row, in which one token's share may be
 // 1e-6, so float32 weights (off by 1e-7, and their sums by more) would decide
 // otherwise than the formula does now and then.  Here
-//   * a weight is 2^(-k/32) (1 + q), k a whole number, |q| < 0.011: k and the
-//     rest of the exponent come from a float32 product and what its rounding left, q
-//     from four terms of the series: roundings of numbers below 2^-6, together at
-//     most 2^-28 of the weight, as likely up as down;
+//   * a weight is 2^(-k/32) (1 + q), k a whole number: k and the rest a / 32 of the
+//     exponent come from a float32 product and what its rounding left, q from four
+//     terms of the series.  |a| <= 1/2, and 1/8 more where the logits' product with
+//     1/T's low part is that large (|max c| near 2^21 below), so |q| < 0.0137; its
+//     roundings, of numbers below 2^-6, are together less than 2^-27 of the weight
+//     (2^-28 where |a| is at most 0.51), as likely up as down;
 //   * sums are of whole numbers: of q in units of 2^-31, with the count, per k (a
-//     bin), or of weights in units of 2^-44.  They do not depend on the order.
+//     bin), or of weights in units of 2^-44, to which each is rounded: one below 2^-45
+//     is kept, but adds nothing.  They do not depend on the order.  u = 0, the first
+//     kept token whatever it weighs, is no matter of sums.
 //
 // A cluster of CTAs takes a row and keeps it in shared memory: one read, a bulk copy
 // per warp.  The cut is found by narrowing: a histogram over k, the bin in which the
@@ -45,7 +49,7 @@ namespace medusa {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048;          // of a histogram; k = 2047: weights below 2^-63, taken as nothing
+constexpr int kBins = 2048;          // of a histogram; k = 2047: weights below 2^-63, nothing in any unit
 constexpr int kTail = kBins - 1;
 constexpr int kIndexBits = 18;       // V <= 2^18
 constexpr int kMaxV = 1 << kIndexBits;
@@ -151,7 +155,7 @@ struct alignas(16) Smem {
   uint64_t warp[kWarps];
   uint64_t loaded[kWarps];  // barriers: a warp's logits are there
   uint64_t row_best[CL], slice[CL], kept_m[CL];  // a word of each CTA of the cluster, which writes it
-  uint32_t row_count[CL], kept_n[CL], listed_by[CL], warp_n[kWarps];
+  uint32_t row_count[CL], kept_n[CL], listed_by[CL], first_by[CL], warp_n[kWarps], warp_first[kWarps];
   uint32_t listed;
   Found found;
   float c, c_low;
@@ -595,6 +599,20 @@ __device__ __noinline__ void draw(const SampleArgs& a, Smem<CL>& s, float* zs, c
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   kept = __reduce_add_sync(0xffffffffu, kept);
+  // u = 0: the first kept token, also where its weight is nothing in the sums' units.
+  // (With top-p none weighs so little: up to 2^18 tokens share more than 2^-24 from the
+  // last kept one on, and those before it weigh more.)
+  if (u == 0.f) {
+    const double least = (double)sc.max - (double)T0 * 745.13321910194122;  // the weight is 2^-1075: 0 in 64 bits
+    uint32_t first = ~0u;
+    for (int i = w0 + lane; i < w1 && first == ~0u; i += 32) {
+      float q;
+      const uint32_t on = __ballot_sync(
+          0xffffffffu, is_kept(zs[i], i) && (zs[i] == sc.max || (double)zs[i] > least) && weight_of<NEAR>(sc, zs[i], q) <= k_cut);
+      if (on) first = (uint32_t)(i0 + i - lane + __ffs(on) - 1);
+    }
+    if (lane == 0) s.warp_first[warp] = first;
+  }
   if (lane == 0) {
     s.warp[warp] = sum;
     s.warp_n[warp] = kept;
@@ -614,6 +632,10 @@ __device__ __noinline__ void draw(const SampleArgs& a, Smem<CL>& s, float* zs, c
     tell<CL>(s.kept_m, t, rank, own);
     tell<CL>(s.kept_n, t, rank, kept);
   }
+  if (u == 0.f && warp == 0) {
+    const uint32_t least = __reduce_min_sync(0xffffffffu, lane < kWarps ? s.warp_first[lane] : ~0u);
+    if (lane < CL) tell<CL>(s.first_by, lane, rank, least);
+  }
   sync_all<CL>();  // the last words that CTAs exchange
   kept = 0;
 #pragma unroll
@@ -621,6 +643,21 @@ __device__ __noinline__ void draw(const SampleArgs& a, Smem<CL>& s, float* zs, c
     if (r < rank) before += s.kept_m[r];
     total += s.kept_m[r];
     kept += s.kept_n[r];
+  }
+  if (u == 0.f) {
+    uint32_t least = ~0u;
+#pragma unroll
+    for (int r = 0; r < CL; ++r) least = min(least, s.first_by[r]);
+    if (s.warp_first[warp] != least) return;  // the token is not this warp's
+    const int i = (int)least - i0;
+    uint64_t w = 0;
+    add(w, zs[i], i);
+    if (lane == 0) {
+      a.token[row] = (int)least;
+      if (a.kept) a.kept[row] = (int)kept;
+      if (a.logp) a.logp[row] = log_share(zs[i], w, total);
+    }
+    return;
   }
   const uint64_t mark = __umul64hi(share_of(u), total);
   if (sum == 0 || before > mark || before + sum <= mark) return;
