@@ -76,7 +76,8 @@ class DecodeLoop:
     page_size the cache is paged: the sequences' tokens, the same as in the
     dense slabs, lie in pages of that many tokens, taken as the steps need them
     (window, sinks: as VerifyStep's).  With `sample` (as VerifyStep's) the roots are
-    drawn, with the numbers that step() is given."""
+    drawn, with the numbers that step() is given: each serves one step, and a step
+    without new ones sets err (TOKEN)."""
 
     def __init__(self, w: dict, model: StandInModel, tree: M.DeviceTree, n_steps: int, L0: int, x0,
                  device="cuda", heads: str = "fused", seed: int = 0, page_size: int | None = None,
@@ -100,7 +101,7 @@ class DecodeLoop:
                                cache="paged" if page_size else "dense", window=window, sinks=sinks, sample=sample)
         self.x = {"q": qkv, "k_new": qkv, "v_new": qkv, "hidden": self.hidden, "tokens": self.st.next_tokens}
         if sample is not None:
-            self.x["uniforms"] = torch.zeros(B, dtype=torch.float32, device=device)
+            self.x["uniforms"] = torch.full((B,), float("nan"), dtype=torch.float32, device=device)
         if page_size:
             self._into_pages(kc.view(B, cap, H, Dh), vc.view(B, cap, H, Dh), L0, cap, page_size)
         else:
@@ -150,7 +151,7 @@ class DecodeLoop:
 
     def step(self, stream=None, side_stream=None, heads_stream=None, uniforms=None):
         """One step; uniforms [B]: the numbers its roots are drawn with (left out: those in x["uniforms"], which a
-        captured step reads)."""
+        captured step reads).  x["uniforms"] is NaN after it."""
         st = self.st
         main = stream if stream is not None else torch.cuda.current_stream()
         if uniforms is not None:
@@ -158,6 +159,9 @@ class DecodeLoop:
                 self.x["uniforms"].copy_(uniforms)
         M.medusa_standin_embed(st.next_tokens, self.model.E, self.hidden, st.err, main)
         st.run(self.x, main, side_stream=side_stream, heads_stream=heads_stream, append=(self.out, self.out_len))
+        if st.sample is not None:  # used: not drawn with again unnoticed
+            with torch.cuda.stream(main):
+                self.x["uniforms"].fill_(float("nan"))
 
     def emitted(self):
         """Per sequence, the tokens emitted so far (host)."""
