@@ -875,14 +875,21 @@ size_t medusa_paged_attn_shared_workspace_size(int B, int n_groups,
  *   common:      device [n_groups], medusa_pages_common's (or less; 0 shares
  *                nothing).
  * The common tokens are read through one of the group's rows; that the others name
- * the same pages is not looked at.  Groups change what is read, not what is
- * computed: one whose common[g] is below 0 or above the length of a row of it
+ * the same pages is not looked at.  Groups change what is read, and in which order it
+ * is added: one whose common[g] is below 0 or above the length of a row of it
  * shares nothing, and where group_start is wrong nobody does (both
- * MEDUSA_DEVERR_LENGTH).  Sharing has its price in launches: a call whose B rows are
- * too short to save as much reading (by max_pages; 128 MB for single tokens) does not
- * look at its groups, and fewer than 128 common tokens are not shared.  Other arguments, results, errors and the workspace's rules
- * are medusa_paged_attn's, its roundings too (the weights go by max_new there and
- * here); the limit on non-finite values holds for one sequence's tokens, as there. */
+ * MEDUSA_DEVERR_LENGTH, if the call looks at its groups).  Sharing has its price in
+ * launches and in writing the common parts.  The host weighs it against what B rows of
+ * max_pages could save (128 MB of reading for single tokens) and, where that is less,
+ * makes the plain call, which does not look at the groups.  It does not know how
+ * long the rows are: with room for long rows, short ones share at a loss (4 tokens
+ * behind 1024, 32 heads of 128, 23 us in a table as wide as they are, 32 in one of
+ * 32768 tokens a row; chunks of 65, 16 of them, 87 and 124), and a caller who knows
+ * them to be short, or to have nothing in common, calls medusa_paged_attn.  Fewer than
+ * 128 common tokens are not shared.  Other arguments, results, errors and the
+ * workspace's rules are medusa_paged_attn's, its roundings too (the weights go by
+ * max_new there and here); the limit on non-finite values holds for one sequence's
+ * tokens, as there. */
 int medusa_paged_attn_shared(const void* q, int64_t q_stride,
                              const void* k_new, int64_t k_stride,
                              const void* v_new, int64_t v_stride,

@@ -21,19 +21,23 @@ namespace {
 // 1030 us for 32768 tokens of 4 heads, 572 and 571 for 8192 of 32 heads; 51 and
 // 40 us for 260 of 32.
 constexpr int kPrepThreads = 256;
-// Sharing takes three launches more than one call's one or two, 15 to 20 us, writes
+// Sharing takes three launches more than one call's one or two, 10 to 20 us, writes
 // the rows' common parts and reads them, and pays where it saves as much reading.
 // Single tokens, us shared and in one launch: 4 behind 1024, 32 heads of 128 (50 MB
-// saved) 34 and 22; 8 (117 MB) 33.7 and 32.4; 16 behind 2048, 8 key heads (126 MB)
-// 33.5 and 32.6; 64 behind 512 (132 MB) 38 and 38; 4 behind 4096 (201 MB) 44 and 49.
-// Chunks of 65 tokens, 32 heads of 128: 16 behind 1024 (252 MB) 115 and 85, behind 4096
-// (1007 MB) 170 and 228; 8 behind 4096 (470 MB) 119 and 124: 64 bytes more for each of
-// the outputs' elements.  Float32 chunks, where the arithmetic counts and blocks fill
-// up: 16 times 9 tokens behind 1024 (31 MB) 56 and 52, 8 behind 4096 (59 MB) 75 and 85,
-// 4 times 30 behind 1024 (50 MB) 75 and 91; single tokens (126 MB) 51 and 49.  The host
+// saved) 33 and 25; 8 (117 MB) 35 and 35; 16 behind 2048, 8 key heads (126 MB) 33 and
+// 35; 64 behind 512 (132 MB) 40 and 41; 4 behind 4096 (201 MB) 41 and 52.  Chunks: 16
+// of 16 tokens behind 4096, 8 key heads (252 MB) 68 and 72; of 65 tokens, 32 heads of
+// 128, 16 behind 1024 (252 MB) 128 and 88, behind 2048 (503 MB) 152 and 139, behind
+// 4096 (1007 MB) 194 and 231; 8 behind 4096 (470 MB) 129 and 127, behind 6000 (688 MB)
+// 153 and 171: 64 bytes more for each of the outputs' elements.  (Where the products
+// of a group's many rows bind, that is too little: 4 trees of 65 behind 8192, 403 MB,
+// 143 and 124.)  Float32 chunks, where the arithmetic counts and blocks fill up: 16
+// times 9 tokens behind 1024 (31 MB) 56 and 52, 8 behind 4096 (59 MB) 75 and 85, 4
+// times 30 behind 1024 (50 MB) 75 and 91; single tokens (126 MB) 51 and 49.  The host
 // knows how long the rows may be, not how long they are: a call whose rows' capacity
-// saves less does not look at its groups.  A group whose common tokens fill no two
-// tiles shares nothing.
+// saves less does not look at its groups, and in a table with room for long rows short
+// ones share at that price.  A group whose common tokens fill no two tiles shares
+// nothing.
 int64_t worth_sharing(int total_q, int H, int Dh, bool f32, bool few) {
   return f32 && !few ? 32ll << 20 : (128ll << 20) + (few ? 0 : 64ll * total_q * H * Dh);
 }
@@ -365,8 +369,8 @@ template <int DH, bool FAST>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int block_rows) {
   // The launch after this one may start: this one begins when kCommon has ended, which
   // has waited for the first launch, so it finds that one's results.  (kCommon letting
-  // this one start early: 37 us in place of 32 for four tokens behind 1024, 178 in
-  // place of 185 for 104 behind up to 16384.)
+  // this one start early: 5 us more for four tokens behind 1024, 7 less for 104
+  // behind up to 16384.)
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;\n" ::: "memory");
   constexpr int kQuads = DH / 4;
   const int64_t rows = (int64_t)a.total_q * a.H, e = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;

@@ -59,8 +59,10 @@
 // of the first and last ones, whose unseen values become zeros, and the results'
 // place.  With a window of 2048: 8192 tokens behind 4096, 32 heads of 128, 311 us and
 // 60 for the launch before it, the same 3200 cycles a tile of two lanes as without
-// one (queries in two parts, at the power limit).  64 tokens' 16384 common keys, 32
-// heads, 40 us with the launch that adds the partials.
+// one (queries in two parts, at the power limit).  Trees of 65 rows on eight prefixes
+// up to 16384, 32 heads of 128, with a window of 2048: 90 us with the launch before it.
+// Groups of 64, 20 and 12 single tokens behind 6000 .. 8192, 32 heads of 128 on 8: 41 us
+// (37 with P in one part), and 8 for the launch that adds the partials.
 #pragma once
 
 #include <utility>

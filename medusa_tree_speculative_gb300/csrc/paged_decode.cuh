@@ -47,7 +47,7 @@ using namespace sm100;
 
 constexpr int RB = 16, KT = 64;
 // The tiles that beginning and ending a unit costs.  A kOwn unit also joins the
-// common part (104 tokens behind up to 16384, eight of them alone: 184, 168 and 171 us
+// common part (104 tokens behind up to 16384, eight of them alone: 188, 174 and 178 us
 // at 2, 3 and 5).
 template <Keys KEYS>
 constexpr int kCost = KEYS == kOwn ? 3 : 2;

@@ -30,8 +30,8 @@
 // by counts and 5800 by sums, a pass over 16384 logits 2500 (counts) to 8000
 // (weights).  Bound for many rows by the weights' instructions, about 30 a logit and
 // pass; atomics are not it (three in place of one per logit: 322 and 312 us).
-// Measured: one row of 32000 4.3 us greedy, 9 without cuts, 14 with top-k, 17 with
-// top-p, 20 with both; 320 rows of 128257 (164 MB) 60, 158, 181, 332 and 187 us, 180
+// Measured: one row of 32000 4.2 us greedy, 9.6 without cuts, 14 with top-k, 18 with
+// top-p, 20 with both; 320 rows of 128257 (164 MB) 60, 159, 182, 333 and 187 us, 186
 // with all kinds of settings among the rows.
 // What did not go: sums in 64-bit floats (16 cycles a warp's instruction; 480 us in
 // place of 342), 64-bit atomics (loops; 342 in place of 225), 1024 threads to a CTA

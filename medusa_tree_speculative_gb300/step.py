@@ -79,7 +79,8 @@ class VerifyStep:
                  attn_order: str = "after_lm", attn_splits="auto", cache: str = "dense", window: int | None = None,
                  sinks: int = 0, group_start=None, sample: dict | None = None):
         """window, sinks: cache="paged" only, as medusa_paged_attn_window takes them.  group_start: cache="paged" only,
-        int32 [groups + 1] on the device, the sequences of each group side by side.  sample: temperature, top_k, top_p
+        int32 [groups + 1] on the device, the sequences of each group side by side (for long common prefixes: with short
+        ones in a table of long rows the groups cost more than they save).  sample: temperature, top_k, top_p
         and min_p, each a number or a value per sequence (left out: 1, 0, 1, 0); run() then takes x["uniforms"] [B]."""
         if cache not in ("dense", "paged"):
             raise ValueError(f"cache {cache!r}")
